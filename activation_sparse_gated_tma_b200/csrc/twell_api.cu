@@ -13,6 +13,8 @@
 #include "../../include/twell.h"
 #include "internal.h"
 #include "fused_small.cuh"
+#include "int8_gemm.h"
+#include "rows.h"
 #include "sparse_backward.cuh"
 
 namespace twell {
@@ -114,15 +116,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// bf16 row-major [outer][inner] matrix, box [box_outer][64], 128-byte swizzle,
-// zero fill out of bounds.  Cached by (device, pointer, shape, box).
-twell_status tmap_bf16(const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_outer, CUtensorMap& out) {
-  using Key = std::tuple<int, uintptr_t, uint64_t, uint64_t, uint32_t>;
+// Row-major [outer][inner] matrix of `type` elements of `bytes` bytes, rows
+// ld_bytes apart; box [box_outer][128 bytes], 128-byte swizzle, zero fill out
+// of bounds.  Cached by (device, pointer, shape, stride, type, box).
+twell_status tmap_rows(const void* ptr, CUtensorMapDataType type, uint64_t bytes, uint64_t inner, uint64_t outer,
+                       uint64_t ld_bytes, uint32_t box_outer, CUtensorMap& out) {
+  using Key = std::tuple<int, uintptr_t, uint64_t, uint64_t, uint64_t, int, uint32_t>;
   static std::mutex mu;
   static std::map<Key, CUtensorMap> cache;
   int dev = 0;
   TW_CUDA(cudaGetDevice(&dev));
-  const Key key{dev, reinterpret_cast<uintptr_t>(ptr), inner, outer, box_outer};
+  const Key key{dev, reinterpret_cast<uintptr_t>(ptr), inner, outer, ld_bytes, static_cast<int>(type), box_outer};
   {
     std::lock_guard<std::mutex> lock(mu);
     auto it = cache.find(key);
@@ -134,17 +138,20 @@ twell_status tmap_bf16(const void* ptr, uint64_t inner, uint64_t outer, uint32_t
   auto enc = encode_fn();
   if (!enc) return fail(TWELL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {inner * 2};
-  cuuint32_t box[2] = {64, box_outer};
+  cuuint64_t strides[1] = {ld_bytes};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / bytes), box_outer};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(&out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = enc(&out, type, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(TWELL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
   std::lock_guard<std::mutex> lock(mu);
   if (cache.size() > 4096) cache.clear();
   cache.emplace(key, out);
   return TWELL_OK;
+}
+
+twell_status tmap_bf16(const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_outer, CUtensorMap& out) {
+  return tmap_rows(ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, outer, inner * 2, box_outer, out);
 }
 
 // ---------------------------------------------------------------- buffer layout
@@ -574,6 +581,99 @@ twell_status dense_ffn_impl(const uint16_t* x, const uint16_t* wg_t, const uint1
   TW_CUDA(trace_begin(stream));
   TW_CUDA(launch_down_store(tm_h, tm_wd, g2, p2, nullptr, gemm_grid(M, K, 256, dev.sms, ks2), stream));
   TW_CUDA(trace_end(stream, "dense_down_gemm"));
+  return TWELL_OK;
+}
+
+// ---------------------------------------------------------------- rows of activations
+int type_bytes(int type) { return type == TWELL_F32 ? 4 : type == TWELL_I8 ? 1 : 2; }
+bool floating(int type) { return type == TWELL_F32 || type == TWELL_BF16 || type == TWELL_F16; }
+// A second floating type next to `type`: the same, fp32, or anything next to fp32.
+bool pairs_with(int type, int other) { return floating(other) && (other == type || other == TWELL_F32 || type == TWELL_F32); }
+bool element_aligned(const void* p, int type) {
+  return p && reinterpret_cast<uintptr_t>(p) % static_cast<unsigned>(type_bytes(type)) == 0;
+}
+
+// A matrix argument: non-NULL, on its element's alignment, rows at least `cols` apart.
+twell_status check_rows(const char* name, const void* p, int type, int64_t ld, int cols) {
+  if (!element_aligned(p, type)) return fail(TWELL_ERR_INVALID, "%s must be non-NULL and aligned to its elements", name);
+  if (ld < cols || ld > (int64_t(1) << 40)) return fail(TWELL_ERR_INVALID, "%s's row stride %lld is below its row length %d (or absurd)", name,
+                             static_cast<long long>(ld), cols);
+  return TWELL_OK;
+}
+
+twell_status layer_norm_impl(const void* x, int x_type, int64_t ldx, const void* weight, const void* bias, int w_type,
+                             int M, int D, float eps, void* y, int y_type, int64_t ldy, float* y_scale, float* mean,
+                             float* rstd, cudaStream_t stream) {
+  g_launches = 0;
+  if (M < 0 || D < 1 || D > kLayerNormMaxD)
+    return fail(TWELL_ERR_INVALID, "invalid sizes M=%d D=%d (need M >= 0, 1 <= D <= %d)", M, D, kLayerNormMaxD);
+  if (!floating(x_type) || (y_type != TWELL_I8 && !pairs_with(x_type, y_type)))
+    return fail(TWELL_ERR_INVALID, "unsupported types: x %d, y %d", x_type, y_type);
+  if ((weight || bias) && !floating(w_type)) return fail(TWELL_ERR_INVALID, "unsupported weight type %d", w_type);
+  if (!(eps >= 0.f)) return fail(TWELL_ERR_INVALID, "eps must be >= 0");
+  if (M == 0) return TWELL_OK;
+  twell_status st;
+  if ((st = check_rows("x", x, x_type, ldx, D)) != TWELL_OK) return st;
+  if ((st = check_rows(y_type == TWELL_I8 ? "q" : "y", y, y_type, ldy, D)) != TWELL_OK) return st;
+  if ((weight && !element_aligned(weight, w_type)) || (bias && !element_aligned(bias, w_type)))
+    return fail(TWELL_ERR_INVALID, "weight and bias must be aligned to their elements");
+  if (y_type == TWELL_I8 && !element_aligned(y_scale, TWELL_F32))
+    return fail(TWELL_ERR_INVALID, "scale must be non-NULL and 4-byte aligned");
+  if ((mean && !element_aligned(mean, TWELL_F32)) || (rstd && !element_aligned(rstd, TWELL_F32)))
+    return fail(TWELL_ERR_INVALID, "mean and rstd must be 4-byte aligned");
+  DeviceInfo dev;
+  if ((st = device_info(dev)) != TWELL_OK) return st;
+  LayerNormParams p = {};
+  p.x = x; p.weight = weight; p.bias = bias; p.y = y; p.y_scale = y_scale; p.mean = mean; p.rstd = rstd;
+  p.ldx = ldx; p.ldy = ldy; p.M = M; p.D = D; p.eps = eps;
+  p.x_type = x_type; p.y_type = y_type; p.w_type = w_type;
+  TW_CUDA(trace_begin(stream));
+  TW_CUDA(launch_layer_norm(p, dev.sms, stream));
+  TW_CUDA(trace_end(stream, y_type == TWELL_I8 ? "layer_norm_int8" : "layer_norm"));
+  return TWELL_OK;
+}
+
+// int8 operand of a product: TMA reads it.
+twell_status check_i8(const char* name, const int8_t* p, int64_t ld, int K) {
+  if (!aligned16(p)) return fail(TWELL_ERR_INVALID, "%s must be non-NULL and 16-byte aligned", name);
+  if (ld < K || ld % 16 != 0 || ld > (int64_t(1) << 39))
+    return fail(TWELL_ERR_INVALID, "%s's row stride %lld must be a multiple of 16 and at least K=%d", name,
+                static_cast<long long>(ld), K);
+  return TWELL_OK;
+}
+
+twell_status int8_product(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w, int64_t ldw,
+                          const float* w_scale, const int8_t* w2, int64_t ldw2, const float* w2_scale,
+                          const float* bias, bool gated, int M, int N, int K, void* y, int y_type, int64_t ldy,
+                          cudaStream_t stream) {
+  g_launches = 0;
+  if (M < 0 || N < 1 || K < 1 || K > kI8MaxK)
+    return fail(TWELL_ERR_INVALID, "invalid sizes M=%d N=%d K=%d (need M >= 0, N >= 1, 1 <= K <= %d)", M, N, K, kI8MaxK);
+  if (!floating(y_type)) return fail(TWELL_ERR_INVALID, "unsupported output type %d", y_type);
+  if (M == 0) return TWELL_OK;
+  twell_status st;
+  if ((st = check_i8("x", x, ldx, K)) != TWELL_OK) return st;
+  if ((st = check_i8(gated ? "wg" : "w", w, ldw, K)) != TWELL_OK) return st;
+  if (gated && (st = check_i8("wu", w2, ldw2, K)) != TWELL_OK) return st;
+  if (!element_aligned(x_scale, TWELL_F32) || !element_aligned(w_scale, TWELL_F32) ||
+      (gated && !element_aligned(w2_scale, TWELL_F32)) || (bias && !element_aligned(bias, TWELL_F32)))
+    return fail(TWELL_ERR_INVALID, "scales must be non-NULL, scales and bias 4-byte aligned");
+  if ((st = check_rows(gated ? "h" : "y", y, y_type, ldy, N)) != TWELL_OK) return st;
+  DeviceInfo dev;
+  if ((st = device_info(dev)) != TWELL_OK) return st;
+  const Int8Plan plan = int8_plan(M, N, K, gated, dev.sms);
+  CUtensorMap tm_x, tm_w, tm_w2;
+  if ((st = tmap_rows(x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, M, ldx, plan.token_tile, tm_x)) != TWELL_OK) return st;
+  if ((st = tmap_rows(w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, ldw, kI8ChannelTile, tm_w)) != TWELL_OK) return st;
+  tm_w2 = tm_w;
+  if (gated && (st = tmap_rows(w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, ldw2, kI8ChannelTile, tm_w2)) != TWELL_OK)
+    return st;
+  Int8GemmParams p = {};
+  p.x_scale = x_scale; p.w_scale = w_scale; p.w2_scale = w2_scale; p.bias = bias;
+  p.y = y; p.ldy = ldy; p.M = M; p.N = N; p.K = K; p.y_type = y_type;
+  TW_CUDA(trace_begin(stream));
+  TW_CUDA(launch_int8_gemm(plan, gated, tm_x, tm_w, tm_w2, p, stream));
+  TW_CUDA(trace_end(stream, gated ? "int8_gated" : "int8_linear"));
   return TWELL_OK;
 }
 
@@ -1016,6 +1116,127 @@ twell_status twell_ffn_bwd(const uint16_t* x, const uint16_t* wg_t, const uint16
   TW_CUDA(trace_end(stream, "bwd_slot_dw"));
   g_launches += 4;  // the brackets above hold two dx and four weight-gradient launches
   return TWELL_OK;
+}
+
+twell_status twell_layer_norm_fwd(const void* x, twell_dtype x_type, int64_t ldx, const void* weight, const void* bias,
+                                  twell_dtype w_type, int M, int D, float eps, void* y, twell_dtype y_type, int64_t ldy,
+                                  float* mean, float* rstd, cudaStream_t stream) {
+  if (!floating(y_type)) return g_launches = 0, fail(TWELL_ERR_INVALID, "unsupported output type %d", y_type);
+  return layer_norm_impl(x, x_type, ldx, weight, bias, w_type, M, D, eps, y, y_type, ldy, nullptr, mean, rstd, stream);
+}
+
+twell_status twell_layer_norm_int8(const void* x, twell_dtype x_type, int64_t ldx, const void* weight, const void* bias,
+                                   twell_dtype w_type, int M, int D, float eps, int8_t* q, int64_t ldq, float* scale,
+                                   float* mean, float* rstd, cudaStream_t stream) {
+  return layer_norm_impl(x, x_type, ldx, weight, bias, w_type, M, D, eps, q, TWELL_I8, ldq, scale, mean, rstd, stream);
+}
+
+size_t twell_layer_norm_bwd_scratch_bytes(int M, int D) {
+  DeviceInfo dev;
+  if (M < 1 || D < 1 || D > kLayerNormMaxD || device_info(dev) != TWELL_OK) return 0;
+  return static_cast<size_t>(layer_norm_bwd_parts(M, D, dev.sms)) * 2 * D * sizeof(float);
+}
+
+twell_status twell_layer_norm_bwd(const void* dy, twell_dtype dy_type, int64_t lddy, const void* x, twell_dtype x_type,
+                                  int64_t ldx, const float* mean, const float* rstd, const void* weight,
+                                  twell_dtype w_type, int M, int D, void* dx, int64_t lddx, float* dweight, float* dbias,
+                                  void* scratch, size_t scratch_bytes, cudaStream_t stream) {
+  g_launches = 0;
+  if (M < 0 || D < 1 || D > kLayerNormMaxD)
+    return fail(TWELL_ERR_INVALID, "invalid sizes M=%d D=%d (need M >= 0, 1 <= D <= %d)", M, D, kLayerNormMaxD);
+  if (!floating(x_type) || !pairs_with(x_type, dy_type))
+    return fail(TWELL_ERR_INVALID, "unsupported types: x %d, dy %d", x_type, dy_type);
+  if (weight && !floating(w_type)) return fail(TWELL_ERR_INVALID, "unsupported weight type %d", w_type);
+  if ((dweight && !element_aligned(dweight, TWELL_F32)) || (dbias && !element_aligned(dbias, TWELL_F32)))
+    return fail(TWELL_ERR_INVALID, "dweight and dbias must be 4-byte aligned");
+  if (M == 0) {
+    if (dweight) TW_CUDA(cudaMemsetAsync(dweight, 0, static_cast<size_t>(D) * sizeof(float), stream));
+    if (dbias) TW_CUDA(cudaMemsetAsync(dbias, 0, static_cast<size_t>(D) * sizeof(float), stream));
+    return TWELL_OK;
+  }
+  twell_status st;
+  if ((st = check_rows("dy", dy, dy_type, lddy, D)) != TWELL_OK) return st;
+  if ((st = check_rows("x", x, x_type, ldx, D)) != TWELL_OK) return st;
+  if ((st = check_rows("dx", dx, x_type, lddx, D)) != TWELL_OK) return st;
+  if (!element_aligned(mean, TWELL_F32) || !element_aligned(rstd, TWELL_F32))
+    return fail(TWELL_ERR_INVALID, "mean and rstd must be non-NULL and 4-byte aligned");
+  if (weight && !element_aligned(weight, w_type)) return fail(TWELL_ERR_INVALID, "weight must be aligned to its elements");
+  const bool sums = dweight || dbias;
+  if (sums && !aligned16(scratch)) return fail(TWELL_ERR_INVALID, "scratch must be non-NULL and 16-byte aligned");
+  DeviceInfo dev;
+  if ((st = device_info(dev)) != TWELL_OK) return st;
+  const int parts = layer_norm_bwd_parts(M, D, dev.sms);
+  const size_t need = static_cast<size_t>(parts) * 2 * D * sizeof(float);
+  if (sums && scratch_bytes < need)
+    return fail(TWELL_ERR_INVALID, "scratch too small: %zu < %zu bytes", scratch_bytes, need);
+  LayerNormBwdParams p = {};
+  p.dy = dy; p.x = x; p.weight = weight; p.mean = mean; p.rstd = rstd; p.dx = dx;
+  p.partial = sums ? static_cast<float*>(scratch) : nullptr;
+  p.dweight = dweight; p.dbias = dbias;
+  p.lddy = lddy; p.ldx = ldx; p.lddx = lddx; p.M = M; p.D = D;
+  p.dy_type = dy_type; p.x_type = x_type; p.w_type = w_type;
+  TW_CUDA(trace_begin(stream));
+  TW_CUDA(launch_layer_norm_bwd(p, dev.sms, stream));
+  TW_CUDA(trace_end(stream, "layer_norm_bwd"));
+  if (sums) {
+    TW_CUDA(trace_begin(stream));
+    TW_CUDA(launch_layer_norm_bwd_reduce(p, parts, stream));
+    TW_CUDA(trace_end(stream, "layer_norm_bwd_reduce"));
+  }
+  return TWELL_OK;
+}
+
+twell_status twell_quantize_rows(const void* x, twell_dtype x_type, int64_t ldx, int M, int K, int8_t* q, int64_t ldq,
+                                 float* scale, cudaStream_t stream) {
+  g_launches = 0;
+  if (M < 0 || K < 1 || K > kI8MaxK)
+    return fail(TWELL_ERR_INVALID, "invalid sizes M=%d K=%d (need M >= 0, 1 <= K <= %d)", M, K, kI8MaxK);
+  if (!floating(x_type)) return fail(TWELL_ERR_INVALID, "unsupported type %d", x_type);
+  if (M == 0) return TWELL_OK;
+  twell_status st;
+  if ((st = check_rows("x", x, x_type, ldx, K)) != TWELL_OK) return st;
+  if ((st = check_rows("q", q, TWELL_I8, ldq, K)) != TWELL_OK) return st;
+  if (!element_aligned(scale, TWELL_F32)) return fail(TWELL_ERR_INVALID, "scale must be non-NULL and 4-byte aligned");
+  DeviceInfo dev;
+  if ((st = device_info(dev)) != TWELL_OK) return st;
+  const QuantizeParams p{x, q, scale, ldx, ldq, M, K, x_type};
+  TW_CUDA(trace_begin(stream));
+  TW_CUDA(launch_quantize_rows(p, dev.sms, stream));
+  TW_CUDA(trace_end(stream, "quantize_rows"));
+  return TWELL_OK;
+}
+
+twell_status twell_dequantize_rows(const int8_t* q, int64_t ldq, const float* scale, int M, int K, void* y,
+                                   twell_dtype y_type, int64_t ldy, cudaStream_t stream) {
+  g_launches = 0;
+  if (M < 0 || K < 1 || K > kI8MaxK)
+    return fail(TWELL_ERR_INVALID, "invalid sizes M=%d K=%d (need M >= 0, 1 <= K <= %d)", M, K, kI8MaxK);
+  if (!floating(y_type)) return fail(TWELL_ERR_INVALID, "unsupported type %d", y_type);
+  if (M == 0) return TWELL_OK;
+  twell_status st;
+  if ((st = check_rows("q", q, TWELL_I8, ldq, K)) != TWELL_OK) return st;
+  if ((st = check_rows("y", y, y_type, ldy, K)) != TWELL_OK) return st;
+  if (!element_aligned(scale, TWELL_F32)) return fail(TWELL_ERR_INVALID, "scale must be non-NULL and 4-byte aligned");
+  DeviceInfo dev;
+  if ((st = device_info(dev)) != TWELL_OK) return st;
+  const QuantizeParams p{q, y, const_cast<float*>(scale), ldq, ldy, M, K, y_type};
+  TW_CUDA(trace_begin(stream));
+  TW_CUDA(launch_dequantize_rows(p, dev.sms, stream));
+  TW_CUDA(trace_end(stream, "dequantize_rows"));
+  return TWELL_OK;
+}
+
+twell_status twell_int8_linear(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w, int64_t ldw,
+                               const float* w_scale, const float* bias, int M, int N, int K, void* y,
+                               twell_dtype y_type, int64_t ldy, cudaStream_t stream) {
+  return int8_product(x, ldx, x_scale, w, ldw, w_scale, nullptr, 0, nullptr, bias, false, M, N, K, y, y_type, ldy, stream);
+}
+
+twell_status twell_int8_gated(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* wg, int64_t ldwg,
+                              const float* wg_scale, const int8_t* wu, int64_t ldwu, const float* wu_scale, int M, int N,
+                              int K, void* h, twell_dtype h_type, int64_t ldh, cudaStream_t stream) {
+  return int8_product(x, ldx, x_scale, wg, ldwg, wg_scale, wu, ldwu, wu_scale, nullptr, true, M, N, K, h, h_type, ldh,
+                      stream);
 }
 
 twell_status dense_ffn_fwd(const uint16_t* x, const uint16_t* wg_t, const uint16_t* wu_t, const uint16_t* wd, int M,

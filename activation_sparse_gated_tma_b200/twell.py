@@ -6,10 +6,11 @@ library is missing or the device is not an sm_100 GPU, calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
-from typing import Dict, Optional
+from typing import Dict, NamedTuple, Optional, Tuple
 
 import torch
 
@@ -55,6 +56,7 @@ def lib() -> ctypes.CDLL:
         raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m activation_sparse_gated_tma_b200.build`")
     L = ctypes.CDLL(LIB_PATH)
     P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    LL, F = ctypes.c_longlong, ctypes.c_float
     IP = ctypes.POINTER(ctypes.c_int)
     BP = ctypes.POINTER(_TwellBuf)
     sig = {
@@ -67,6 +69,14 @@ def lib() -> ctypes.CDLL:
         "twell_ffn_bwd": (I, [P, P, P, P, BP, P, I, P, P, P, P, P, S, P]),
         "twell_bwd_slot_route": (I, [I]),
         "twell_read_status": (I, [BP, IP, IP, P]),
+        "twell_layer_norm_fwd": (I, [P, I, LL, P, P, I, I, I, F, P, I, LL, P, P, P]),
+        "twell_layer_norm_int8": (I, [P, I, LL, P, P, I, I, I, F, P, LL, P, P, P, P]),
+        "twell_layer_norm_bwd_scratch_bytes": (S, [I, I]),
+        "twell_layer_norm_bwd": (I, [P, I, LL, P, I, LL, P, P, P, I, I, I, P, LL, P, P, P, S, P]),
+        "twell_quantize_rows": (I, [P, I, LL, I, I, P, LL, P, P]),
+        "twell_dequantize_rows": (I, [P, LL, P, I, I, P, I, LL, P]),
+        "twell_int8_linear": (I, [P, LL, P, P, LL, P, P, I, I, I, P, I, LL, P]),
+        "twell_int8_gated": (I, [P, LL, P, P, LL, P, P, LL, P, I, I, I, P, I, LL, P]),
         "dense_ffn_fwd": (I, [P, P, P, P, I, I, I, P, P, P]),
         "dense_ffn_fwd_bf16h": (I, [P, P, P, P, I, I, I, P, P, P]),
         "dense_ffn_fwd_noalloc": (I, [P, P, P, P, I, I, I, P, P]),
@@ -348,6 +358,254 @@ def dense_ffn_noalloc(x: torch.Tensor, wg_t: torch.Tensor, wu_t: torch.Tensor, w
     return y
 
 
+# ---------------------------------------------------------------------------
+# Rows of activations: layer norm, its backward pass, int8 rows and products.
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.int8: 3}  # twell_dtype
+_FLOATING = (torch.float32, torch.bfloat16, torch.float16)
+_I8 = (torch.int8,)
+_HERE = contextlib.nullcontext()
+
+
+def _where(stream, *tensors):
+    """(stream handle, context) of a call on `tensors`: their common CUDA
+    device made current, and a given stream too, so that what the call
+    allocates belongs to the stream it runs on."""
+    device = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, not {device}")
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream on {stream.device}, tensors on {device}")
+        return stream.cuda_stream, torch.cuda.stream(stream)
+    s = torch.cuda.current_stream(device).cuda_stream
+    return s, (_HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device))
+
+
+def _rows(t: torch.Tensor, name: str, dtypes, shape=None) -> int:
+    """Row stride of a matrix argument (rows may be strided, elements not)."""
+    if t.dim() != 2 or t.dtype not in dtypes or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be a matrix{'' if shape is None else f' of shape {tuple(shape)}'} of "
+                         f"{' or '.join(map(str, dtypes))}, got {t.dtype} {tuple(t.shape)}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s elements of a row must be contiguous (strides {t.stride()})")
+    if rows <= 1:  # the stride of a single row says nothing
+        return -(-cols // 16) * 16
+    if t.stride(0) < cols:
+        raise ValueError(f"{name}'s rows overlap (strides {t.stride()})")
+    return t.stride(0)
+
+
+def _vector(t: Optional[torch.Tensor], name: str, n: int, dtypes=(torch.float32,)) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype not in dtypes or tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} {' or '.join(map(str, dtypes))}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _affine(weight, bias, D):
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError(f"weight and bias must have one type, got {weight.dtype} and {bias.dtype}")
+    ref = weight if weight is not None else bias
+    return (_vector(weight, "weight", D, _FLOATING), _vector(bias, "bias", D, _FLOATING),
+            0 if ref is None else _DTYPES[ref.dtype])
+
+
+def _int8_rows(M: int, K: int, device) -> torch.Tensor:
+    """int8 [M][K] whose row stride is a multiple of 16, as the products need it."""
+    ld = -(-K // 16) * 16
+    q = torch.empty((M, ld), dtype=torch.int8, device=device)
+    return q if ld == K else q[:, :K]
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+               stats: bool = False, stream=None):
+    """twell_layer_norm_fwd: y = (x - mean) rstd weight + bias over the rows of x [M][D].
+
+    out_dtype (default x's) is x's type, float32, or any of the three when x is
+    float32; `out` gives the output, whose rows may be strided.  With
+    stats=True returns (y, mean, rstd), what layer_norm_bwd needs."""
+    ldx = _rows(x, "x", _FLOATING)
+    M, D = x.shape
+    w, b, wt = _affine(weight, bias, D)
+    if out is not None and out_dtype not in (None, out.dtype):
+        raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    s, ctx = _where(stream, x, weight, bias, out)
+    with ctx:
+        if out is None:
+            out = torch.empty((M, D), dtype=out_dtype or x.dtype, device=x.device)
+        ldy = _rows(out, "out", _FLOATING, (M, D))
+        mean = rstd = None
+        if stats:
+            mean = torch.empty(M, dtype=torch.float32, device=x.device)
+            rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+        _check(lib().twell_layer_norm_fwd(x.data_ptr(), _DTYPES[x.dtype], ldx, w, b, wt, M, D, eps, out.data_ptr(),
+                                          _DTYPES[out.dtype], ldy, mean.data_ptr() if stats else None,
+                                          rstd.data_ptr() if stats else None, s), "twell_layer_norm_fwd")
+    return (out, mean, rstd) if stats else out
+
+
+def layer_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                    eps: float = 1e-5, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """twell_layer_norm_int8: the norm of x's rows as int8 rows and their scales,
+    (q [M][D], scale [M]), ready for int8_linear and int8_gated."""
+    ldx = _rows(x, "x", _FLOATING)
+    M, D = x.shape
+    w, b, wt = _affine(weight, bias, D)
+    s, ctx = _where(stream, x, weight, bias)
+    with ctx:
+        q = _int8_rows(M, D, x.device)
+        scale = torch.empty(M, dtype=torch.float32, device=x.device)
+        _check(lib().twell_layer_norm_int8(x.data_ptr(), _DTYPES[x.dtype], ldx, w, b, wt, M, D, eps, q.data_ptr(),
+                                           q.stride(0), scale.data_ptr(), None, None, s), "twell_layer_norm_int8")
+    return q, scale
+
+
+def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                   weight: Optional[torch.Tensor] = None, param_grads: bool = True,
+                   scratch: Optional[torch.Tensor] = None, stream=None):
+    """twell_layer_norm_bwd: (dx, dweight, dbias) from the forward's input, mean
+    and rstd and the upstream gradient dy (x's type, float32, or any of the
+    three when x is float32).  dx is of x's type, the parameters' gradients are
+    float32 (None with param_grads=False)."""
+    ldx = _rows(x, "x", _FLOATING)
+    M, D = x.shape
+    lddy = _rows(dy, "dy", _FLOATING, (M, D))
+    w = _vector(weight, "weight", D, _FLOATING)
+    s, ctx = _where(stream, x, dy, mean, rstd, weight, scratch)
+    L = lib()
+    with ctx:
+        dx = torch.empty((M, D), dtype=x.dtype, device=x.device)
+        dw = db = None
+        need = 0
+        if param_grads:
+            dw = torch.empty(D, dtype=torch.float32, device=x.device)
+            db = torch.empty(D, dtype=torch.float32, device=x.device)
+            need = L.twell_layer_norm_bwd_scratch_bytes(M, D)
+            if scratch is None:
+                scratch = torch.empty(need, dtype=torch.uint8, device=x.device)
+            elif not scratch.is_contiguous():
+                raise ValueError("scratch must be contiguous")
+        _check(L.twell_layer_norm_bwd(dy.data_ptr(), _DTYPES[dy.dtype], lddy, x.data_ptr(), _DTYPES[x.dtype], ldx,
+                                      _vector(mean, "mean", M), _vector(rstd, "rstd", M), w,
+                                      0 if weight is None else _DTYPES[weight.dtype], M, D, dx.data_ptr(),
+                                      _rows(dx, "dx", _FLOATING), dw.data_ptr() if param_grads else None,
+                                      db.data_ptr() if param_grads else None,
+                                      scratch.data_ptr() if param_grads else None,
+                                      scratch.numel() * scratch.element_size() if param_grads else 0, s),
+               "twell_layer_norm_bwd")
+    return dx, dw, db
+
+
+def quantize_rows(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """twell_quantize_rows: (q int8 [M][K], scale [M]) with x ~ q scale; for
+    activations (a scale per token) and weights [N][K] (one per channel)."""
+    ldx = _rows(x, "x", _FLOATING)
+    M, K = x.shape
+    s, ctx = _where(stream, x)
+    with ctx:
+        q = _int8_rows(M, K, x.device)
+        scale = torch.empty(M, dtype=torch.float32, device=x.device)
+        _check(lib().twell_quantize_rows(x.data_ptr(), _DTYPES[x.dtype], ldx, M, K, q.data_ptr(), q.stride(0),
+                                         scale.data_ptr(), s), "twell_quantize_rows")
+    return q, scale
+
+
+def dequantize_rows(q: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
+                    stream=None) -> torch.Tensor:
+    """twell_dequantize_rows: q scale, of out_dtype."""
+    ldq = _rows(q, "q", _I8)
+    M, K = q.shape
+    if out_dtype not in _FLOATING:
+        raise ValueError(f"out_dtype must be one of {_FLOATING}, got {out_dtype}")
+    s, ctx = _where(stream, q, scale)
+    with ctx:
+        y = torch.empty((M, K), dtype=out_dtype, device=q.device)
+        _check(lib().twell_dequantize_rows(q.data_ptr(), ldq, _vector(scale, "scale", M), M, K, y.data_ptr(),
+                                           _DTYPES[out_dtype], K, s), "twell_dequantize_rows")
+    return y
+
+
+def int8_linear(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """twell_int8_linear: y [M][N] = x w^T x_scale w_scale (+ bias) from int8
+    rows x [M][K] and w [N][K] (bases 16-byte aligned, row strides multiples of
+    16, as quantize_rows makes them)."""
+    ldx, ldw = _rows(x, "x", _I8), _rows(w, "w", _I8)
+    (M, K), N = x.shape, w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"x {tuple(x.shape)} and w {tuple(w.shape)} must have rows of one length")
+    if out is None and out_dtype not in _FLOATING:
+        raise ValueError(f"out_dtype must be one of {_FLOATING}, got {out_dtype}")
+    s, ctx = _where(stream, x, x_scale, w, w_scale, bias, out)
+    with ctx:
+        y = torch.empty((M, N), dtype=out_dtype, device=x.device) if out is None else out
+        _check(lib().twell_int8_linear(x.data_ptr(), ldx, _vector(x_scale, "x_scale", M), w.data_ptr(), ldw,
+                                       _vector(w_scale, "w_scale", N), _vector(bias, "bias", N), M, N, K, y.data_ptr(),
+                                       _DTYPES.get(y.dtype, -1), _rows(y, "out", _FLOATING, (M, N)), s),
+               "twell_int8_linear")
+    return y
+
+
+def int8_gated(x: torch.Tensor, x_scale: torch.Tensor, wg: torch.Tensor, wg_scale: torch.Tensor, wu: torch.Tensor,
+               wu_scale: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """twell_int8_gated: h [M][N] = u ReLU(g) with g, u the int8 products of x
+    with wg and wu (operands as for int8_linear)."""
+    ldx, ldg = _rows(x, "x", _I8), _rows(wg, "wg", _I8)
+    (M, K), N = x.shape, wg.shape[0]
+    if wg.shape[1] != K:
+        raise ValueError(f"x {tuple(x.shape)} and wg {tuple(wg.shape)} must have rows of one length")
+    ldu = _rows(wu, "wu", _I8, (N, K))
+    if out is None and out_dtype not in _FLOATING:
+        raise ValueError(f"out_dtype must be one of {_FLOATING}, got {out_dtype}")
+    s, ctx = _where(stream, x, x_scale, wg, wg_scale, wu, wu_scale, out)
+    with ctx:
+        h = torch.empty((M, N), dtype=out_dtype, device=x.device) if out is None else out
+        _check(lib().twell_int8_gated(x.data_ptr(), ldx, _vector(x_scale, "x_scale", M), wg.data_ptr(), ldg,
+                                      _vector(wg_scale, "wg_scale", N), wu.data_ptr(), ldu,
+                                      _vector(wu_scale, "wu_scale", N), M, N, K, h.data_ptr(),
+                                      _DTYPES.get(h.dtype, -1), _rows(h, "out", _FLOATING, (M, N)), s),
+               "twell_int8_gated")
+    return h
+
+
+class Int8FFN(NamedTuple):
+    """The dense FFN's weights as int8 rows with a scale per output channel:
+    wg, wu [N][K] as in the bf16 layout, wd transposed to [K][N] (each output
+    column of y is one row)."""
+    wg: torch.Tensor
+    wg_scale: torch.Tensor
+    wu: torch.Tensor
+    wu_scale: torch.Tensor
+    wd_t: torch.Tensor
+    wd_scale: torch.Tensor
+
+
+def int8_ffn_weights(wg_t: torch.Tensor, wu_t: torch.Tensor, wd: torch.Tensor) -> Int8FFN:
+    """Quantise the FFN's weights (all [N][K]) once, for dense_ffn_int8."""
+    return Int8FFN(*quantize_rows(wg_t), *quantize_rows(wu_t), *quantize_rows(wd.t().contiguous()))
+
+
+def dense_ffn_int8(x: torch.Tensor, weights: Int8FFN, norm=None, out_dtype: torch.dtype = torch.float32,
+                   stream=None) -> torch.Tensor:
+    """The dense FFN (dense_ffn) in 8-bit integers: x's rows quantised, the
+    gated pair of products, h's rows quantised, the down product.  norm =
+    (weight, bias, eps) applies the layer norm to x first (layer_norm_int8)."""
+    q, s = quantize_rows(x, stream) if norm is None else layer_norm_int8(x, *norm, stream=stream)
+    h = int8_gated(q, s, weights.wg, weights.wg_scale, weights.wu, weights.wu_scale, stream=stream)
+    q, s = quantize_rows(h, stream)
+    return int8_linear(q, s, weights.wd_t, weights.wd_scale, out_dtype=out_dtype, stream=stream)
+
+
 def bwd_slot_route(route: int) -> None:
     """twell_bwd_slot_route: 0 chooses the slotted rows' backward route by
     their entry count, 1 forces the dense-slot GEMMs, 2 the gather passes
@@ -362,10 +620,16 @@ def test_expire_wait(limit_ns: int) -> None:
 
 
 def sparse_ffn(x: torch.Tensor, wg_t: torch.Tensor, wu_t: torch.Tensor, wd: torch.Tensor, T: int, C: int,
-               tw: Optional[TwellBuffers] = None, y: Optional[torch.Tensor] = None, sync: bool = True):
+               tw: Optional[TwellBuffers] = None, y: Optional[torch.Tensor] = None, sync: bool = True, norm=None):
     """Whole sparse forward: gate_pack (+ one retry with a larger dense-row buffer
-    on capacity overflow, when sync) then ffn_fwd.  Returns (y, tw)."""
+    on capacity overflow, when sync) then ffn_fwd.  Returns (y, tw).
+
+    norm = (weight, bias, eps) applies the layer norm to x first: x may then be
+    float32 or bfloat16, and the FFN runs on its bfloat16 output.  (A weight of
+    0 and a bias of 1 in the last column make it the gate's bias column.)"""
     M, K = x.shape
+    if norm is not None:
+        x = layer_norm(x, *norm, out_dtype=torch.bfloat16)
     N = wg_t.shape[0]
     if tw is None:
         tw = TwellBuffers(M, K, N, T, C, device=x.device)

@@ -21,6 +21,10 @@
  * overflow reported to the host, which retries with larger storage).
  * dense_ffn_fwd computes the same y with dense tensor-core GEMMs.
  *
+ * Around the FFN (second half of this file): the layer norm that feeds it and
+ * that norm's backward pass, and the dense FFN's 8-bit integer form -- rows
+ * quantised to int8, products of int8 rows with a scale per token and channel.
+ *
  * Conventions for every entry point:
  *   - bf16 tensors are passed as uint16_t bit patterns; all matrices are
  *     row-major and contiguous; every pointer must be 16-byte aligned.
@@ -271,6 +275,97 @@ twell_status dense_ffn_fwd_bf16h(const uint16_t* x, const uint16_t* wg_t, const 
  */
 twell_status dense_ffn_fwd_noalloc(const uint16_t* x, const uint16_t* wg_t, const uint16_t* wu_t, const uint16_t* wd,
                                    int M, int K, int N, float* y, cudaStream_t stream);
+
+/*
+ * ------------------------------------------------------------ rows of activations
+ * Conventions of the calls from here to twell_int8_gated, beyond those above:
+ *   - a matrix argument is a pointer, and a row stride `ld*` in elements (at
+ *     least the row length); a row's elements are contiguous.  Pointers need
+ *     only their element's alignment unless a call says more; rows whose base
+ *     and stride are multiples of 16 bytes take 16-byte accesses.
+ *   - outputs are overwritten and must not overlap inputs; bytes between rows
+ *     are neither read nor written.
+ *   - M = 0 is valid and launches nothing.
+ *   - repeated calls on one device give the same bits.
+ */
+typedef enum { TWELL_F32 = 0, TWELL_BF16 = 1, TWELL_F16 = 2, TWELL_I8 = 3 } twell_dtype;
+
+/*
+ * Layer norm over rows of D elements, 1 <= D <= 16384:
+ *   mean = sum x / D, rstd = 1 / sqrt(sum (x - mean)^2 / D + eps),
+ *   y = (x - mean) rstd weight + bias.
+ * weight, bias [D] of w_type (F32, BF16, F16), or NULL for ones and zeros;
+ * mean, rstd [M] fp32 outputs, or NULL.  All arithmetic is fp32; y is rounded
+ * once.  y_type is x_type, or F32, or (x_type F32) any floating type.  The FFN's
+ * rows with the gate bias in column K-1 are the outputs of D = K-1, ldy = K (that
+ * column is then left alone), or of D = K with weight[K-1] = 0, bias[K-1] = 1.
+ */
+twell_status twell_layer_norm_fwd(const void* x, twell_dtype x_type, int64_t ldx, const void* weight, const void* bias,
+                                  twell_dtype w_type, int M, int D, float eps, void* y, twell_dtype y_type, int64_t ldy,
+                                  float* mean, float* rstd, cudaStream_t stream);
+
+/*
+ * The same norm with its rows quantised as by twell_quantize_rows from their
+ * fp32 values (never rounded to 16 bits in between): q [M][D] int8, scale [M].
+ */
+twell_status twell_layer_norm_int8(const void* x, twell_dtype x_type, int64_t ldx, const void* weight, const void* bias,
+                                   twell_dtype w_type, int M, int D, float eps, int8_t* q, int64_t ldq, float* scale,
+                                   float* mean, float* rstd, cudaStream_t stream);
+
+/*
+ * Backward pass of the norm from its input, the mean and rstd of the forward
+ * and the upstream gradient dy (dy_type: x_type, or F32, or, x_type F32, any):
+ * with xh = (x - mean) rstd and g = dy weight,
+ *   dx = rstd (g - (sum g + xh sum g xh) / D)      of x_type,
+ *   dweight [D] = sum over rows of dy xh, dbias [D] = sum over rows of dy,  fp32.
+ * dweight and dbias may each be NULL.  scratch: device memory of at least
+ * twell_layer_norm_bwd_scratch_bytes(M, D) bytes, 16-byte aligned (one partial
+ * row of both sums per group of rows); unused when both are NULL.  The size
+ * depends on the current device; it is 0 for invalid sizes (and M = 0).  With
+ * M = 0 the parameter gradients are set to zero.
+ */
+size_t twell_layer_norm_bwd_scratch_bytes(int M, int D);
+twell_status twell_layer_norm_bwd(const void* dy, twell_dtype dy_type, int64_t lddy, const void* x, twell_dtype x_type,
+                                  int64_t ldx, const float* mean, const float* rstd, const void* weight,
+                                  twell_dtype w_type, int M, int D, void* dx, int64_t lddx, float* dweight, float* dbias,
+                                  void* scratch, size_t scratch_bytes, cudaStream_t stream);
+
+/*
+ * Rows to int8: with amax the largest magnitude of a row, scale = amax / 127
+ * (fp32) and q = the integer nearest to 127 x / amax, ties to even, so
+ * x ~ q scale and |q| <= 127.  A row of zeros has scale 0 and q = 0; a row
+ * with a NaN or an infinity has scale NaN and q = 0, so that whatever is
+ * computed from it is NaN.  x_type F32, BF16 or F16; 1 <= K <= 131071.
+ * Weights ([N][K], one scale per output channel) are quantised the same way.
+ */
+twell_status twell_quantize_rows(const void* x, twell_dtype x_type, int64_t ldx, int M, int K, int8_t* q, int64_t ldq,
+                                 float* scale, cudaStream_t stream);
+/* y = q scale, of y_type F32, BF16 or F16. */
+twell_status twell_dequantize_rows(const int8_t* q, int64_t ldq, const float* scale, int M, int K, void* y,
+                                   twell_dtype y_type, int64_t ldy, cudaStream_t stream);
+
+/*
+ * Product of int8 rows with a scale per token and per channel:
+ *   y[m][n] = float(sum_k x[m][k] w[n][k]) x_scale[m] w_scale[n]  (+ bias[n])
+ * The sum is exact (32-bit integers, K <= 131071); scaling is fp32 in the order
+ * written and y is rounded once to y_type (F32, BF16, F16).  x [M][K], w [N][K]
+ * int8 (all values -128..127): 16-byte aligned, row strides multiples of 16; K
+ * itself and N may be any number >= 1 (what lies between a row's end and the
+ * next row is not read as data).  bias [N] fp32 or NULL.  No workspace.  Every
+ * wait inside is bounded; a tile whose wait gave up is written as NaN.
+ */
+twell_status twell_int8_linear(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w, int64_t ldw,
+                               const float* w_scale, const float* bias, int M, int N, int K, void* y,
+                               twell_dtype y_type, int64_t ldy, cudaStream_t stream);
+
+/*
+ * The gated pair of such products of the same tokens, h = u ReLU(g) with
+ * g = x wg^T and u = x wu^T scaled as above (h is 0 where g <= 0; NaN scales
+ * give NaN): the first stage of the dense FFN (dense_ffn_fwd) on int8 weights.
+ */
+twell_status twell_int8_gated(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* wg, int64_t ldwg,
+                              const float* wg_scale, const int8_t* wu, int64_t ldwu, const float* wu_scale, int M, int N,
+                              int K, void* h, twell_dtype h_type, int64_t ldh, cudaStream_t stream);
 
 /*
  * Host-side fault injection for tests of the device status path.  Arms a
