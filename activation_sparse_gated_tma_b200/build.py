@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtwell.so")
-SOURCES = ["gemm_kernels.cu", "twell_api.cu", "rows.cu", "int8_gemm.cu"]
+SOURCES = ["gemm_kernels.cu", "twell_api.cu", "rows_norm.cu", "rows_bwd.cu", "rows_int8.cu",
+           "int8_gemm.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3", f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -1,4 +1,4 @@
-// Launch interface of the row kernels (rows.cu): layer norm, its backward
+// Launch interface of the row kernels (rows_*.cu): layer norm, its backward
 // pass, row quantisation to int8 and back.  Not part of the public ABI.
 #pragma once
 
@@ -7,7 +7,33 @@
 
 namespace twell {
 
-constexpr int kLayerNormMaxD = 16384;  // a row stays in the registers of at most 512 threads, 32 elements each
+// Shared memory of one row in a ring slot: its bytes, up to 15 before them, the
+// rest of the last 16 and what a shifted read takes behind it.
+__host__ __device__ constexpr uint32_t row_slot_bytes(uint32_t row_bytes) { return (row_bytes + 46) / 16 * 16; }
+
+constexpr int kRowThreads = 256;     // of a block at most
+constexpr int kMaxGroups = 8;        // rows that a block works on at once
+constexpr int kMaxGroupWarps = 8;    // of a row
+constexpr int kMaxSlots = 8;         // of a ring
+constexpr int kMaxLayers = 20;       // a lane holds up to 80 elements
+constexpr int kMaxBatch = 8;         // rows of a batch, backward
+constexpr int kBwdThreads = 512;     // of a block at most, backward
+constexpr int kLayerNormMaxD = 16384;
+constexpr int kQuantizeMaxRow = 4 * kMaxLayers * kRowThreads;  // longer rows are read twice
+
+// Blocks that share an SM's registers.
+constexpr int row_blocks(int layers) { return layers <= 4 ? 4 : layers <= 8 ? 3 : 2; }
+
+// How a launch lays out rows over blocks (see rows.cuh).  Rows [ring_begin,
+// ring_end) pass through the ring: those whose 16-byte pieces lie inside the matrices.
+struct RowPlan {
+  int warps, slots;
+  uint32_t slot_bytes, ring_begin, ring_end;
+};
+struct BatchPlan {
+  int rows, slots;
+  uint32_t batches, ring_begin, ring_end;
+};
 
 // Rows are `ld` elements apart; a row's elements are contiguous.  Types are
 // twell_dtype values; out_type TWELL_I8 writes quantised rows and y_scale.
@@ -21,7 +47,7 @@ struct LayerNormParams {
   float* rstd;         // [M] or NULL
   int64_t ldx, ldy;
   int M, D;
-  float eps;
+  float eps, inv_d;    // inv_d: 1 / D
   int x_type, y_type, w_type;
 };
 cudaError_t launch_layer_norm(const LayerNormParams& p, int sms, cudaStream_t s);
@@ -38,11 +64,13 @@ struct LayerNormBwdParams {
   float* dbias;        // [D] or NULL
   int64_t lddy, ldx, lddx;
   int M, D;
+  float inv_d;         // 1 / D
   int dy_type, x_type, w_type;
 };
-// Row groups that write a partial sum each (a function of the sizes and the SM count only).
-int layer_norm_bwd_parts(int M, int D, int sms);
-cudaError_t launch_layer_norm_bwd(const LayerNormBwdParams& p, int sms, cudaStream_t s);
+// Most partial rows of the parameter gradients that a call writes.
+int layer_norm_bwd_max_parts(int M, int D, int sms);
+// Returns the partial rows it writes in `parts`.
+cudaError_t launch_layer_norm_bwd(const LayerNormBwdParams& p, int sms, int& parts, cudaStream_t s);
 cudaError_t launch_layer_norm_bwd_reduce(const LayerNormBwdParams& p, int parts, cudaStream_t s);
 
 struct QuantizeParams {
