@@ -24,15 +24,20 @@ struct Int8GemmParams {
   int y_type;
 };
 
-// How a product is cut: tokens per tile and CTAs (a cluster) that share a tile's reduction.
+// How a product is cut: CTA pairs on 256 x 256 tiles, or tiles of 128 channels
+// by `token_tile` tokens whose reduction k_splits CTAs (a cluster) share.
 struct Int8Plan {
+  bool pairs;
   int token_tile;
   int k_splits;
 };
-Int8Plan int8_plan(int M, int N, int K, bool gated, int sms);
+// aligned_rows: the output's rows start on 16 bytes.
+Int8Plan int8_plan(int M, int N, int K, bool gated, bool aligned_rows, int sms);
+// Rows of the boxes of the operands' tensor maps (all kI8BK wide).
+inline int int8_token_box(const Int8Plan& plan) { return plan.pairs ? 128 : plan.token_tile; }
+constexpr int kI8ChannelBox = 128;
 
-// tm_x's box is token_tile rows, tm_w's and tm_w2's kI8ChannelTile rows, all kI8BK wide.
 cudaError_t launch_int8_gemm(const Int8Plan& plan, bool gated, const CUtensorMap& tm_x, const CUtensorMap& tm_w,
-                             const CUtensorMap& tm_w2, const Int8GemmParams& p, cudaStream_t s);
+                             const CUtensorMap& tm_w2, const Int8GemmParams& p, int sms, cudaStream_t s);
 
 }  // namespace twell

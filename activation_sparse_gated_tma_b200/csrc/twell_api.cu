@@ -661,18 +661,19 @@ twell_status int8_product(const int8_t* x, int64_t ldx, const float* x_scale, co
   if ((st = check_rows(gated ? "h" : "y", y, y_type, ldy, N)) != TWELL_OK) return st;
   DeviceInfo dev;
   if ((st = device_info(dev)) != TWELL_OK) return st;
-  const Int8Plan plan = int8_plan(M, N, K, gated, dev.sms);
+  const bool aligned_rows = aligned16(y) && (ldy * type_bytes(y_type)) % 16 == 0;
+  const Int8Plan plan = int8_plan(M, N, K, gated, aligned_rows, dev.sms);
   CUtensorMap tm_x, tm_w, tm_w2;
-  if ((st = tmap_rows(x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, M, ldx, plan.token_tile, tm_x)) != TWELL_OK) return st;
-  if ((st = tmap_rows(w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, ldw, kI8ChannelTile, tm_w)) != TWELL_OK) return st;
+  if ((st = tmap_rows(x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, M, ldx, int8_token_box(plan), tm_x)) != TWELL_OK) return st;
+  if ((st = tmap_rows(w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, ldw, kI8ChannelBox, tm_w)) != TWELL_OK) return st;
   tm_w2 = tm_w;
-  if (gated && (st = tmap_rows(w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, ldw2, kI8ChannelTile, tm_w2)) != TWELL_OK)
+  if (gated && (st = tmap_rows(w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, ldw2, kI8ChannelBox, tm_w2)) != TWELL_OK)
     return st;
   Int8GemmParams p = {};
   p.x_scale = x_scale; p.w_scale = w_scale; p.w2_scale = w2_scale; p.bias = bias;
   p.y = y; p.ldy = ldy; p.M = M; p.N = N; p.K = K; p.y_type = y_type;
   TW_CUDA(trace_begin(stream));
-  TW_CUDA(launch_int8_gemm(plan, gated, tm_x, tm_w, tm_w2, p, stream));
+  TW_CUDA(launch_int8_gemm(plan, gated, tm_x, tm_w, tm_w2, p, dev.sms, stream));
   TW_CUDA(trace_end(stream, gated ? "int8_gated" : "int8_linear"));
   return TWELL_OK;
 }

@@ -6,7 +6,6 @@ library is missing or the device is not an sm_100 GPU, calls raise.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -364,46 +363,56 @@ def dense_ffn_noalloc(x: torch.Tensor, wg_t: torch.Tensor, wu_t: torch.Tensor, w
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.int8: 3}  # twell_dtype
 _FLOATING = (torch.float32, torch.bfloat16, torch.float16)
 _I8 = (torch.int8,)
-_HERE = contextlib.nullcontext()
 
 
-def _where(stream, *tensors):
-    """(stream handle, context) of a call on `tensors`: their common CUDA
-    device made current, and a given stream too, so that what the call
-    allocates belongs to the stream it runs on."""
-    device = tensors[0].device
+def _elsewhere(stream, *tensors) -> bool:
+    """Whether a call on `tensors` (on one CUDA device) has to change the
+    current device or stream first; small calls are bound by the host, so the
+    usual case does neither."""
+    d = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, not {device}")
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream on {stream.device}, tensors on {device}")
-        return stream.cuda_stream, torch.cuda.stream(stream)
-    s = torch.cuda.current_stream(device).cuda_stream
-    return s, (_HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device))
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"tensors on {tensors[0].device} and {t.device}")
+    if d < 0:
+        raise ValueError(f"tensors must be on a CUDA device, not {tensors[0].device}")
+    return stream is not None or d != torch.cuda.current_device()
+
+
+def _there(stream, t: torch.Tensor):
+    """Context of such a call: the tensors' device made current, and a given
+    stream too, so that what the call allocates belongs to the stream it runs on."""
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise ValueError(f"stream on {stream.device}, tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _here(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _rows(t: torch.Tensor, name: str, dtypes, shape=None) -> int:
     """Row stride of a matrix argument (rows may be strided, elements not)."""
-    if t.dim() != 2 or t.dtype not in dtypes or (shape is not None and tuple(t.shape) != tuple(shape)):
+    size = t.shape
+    if len(size) != 2 or t.dtype not in dtypes or (shape is not None and size != shape):
         raise ValueError(f"{name} must be a matrix{'' if shape is None else f' of shape {tuple(shape)}'} of "
-                         f"{' or '.join(map(str, dtypes))}, got {t.dtype} {tuple(t.shape)}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+                         f"{' or '.join(map(str, dtypes))}, got {t.dtype} {tuple(size)}")
+    rows, cols = size
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name}'s elements of a row must be contiguous (strides {t.stride()})")
     if rows <= 1:  # the stride of a single row says nothing
         return -(-cols // 16) * 16
-    if t.stride(0) < cols:
+    if ld < cols:
         raise ValueError(f"{name}'s rows overlap (strides {t.stride()})")
-    return t.stride(0)
+    return ld
 
 
 def _vector(t: Optional[torch.Tensor], name: str, n: int, dtypes=(torch.float32,)) -> Optional[int]:
     if t is None:
         return None
-    if t.dtype not in dtypes or tuple(t.shape) != (n,) or not t.is_contiguous():
+    if t.dtype not in dtypes or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} {' or '.join(map(str, dtypes))}, "
                          f"got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
@@ -417,11 +426,15 @@ def _affine(weight, bias, D):
             0 if ref is None else _DTYPES[ref.dtype])
 
 
-def _int8_rows(M: int, K: int, device) -> torch.Tensor:
+def _matrix(M: int, N: int, dtype, like: torch.Tensor) -> torch.Tensor:
+    return torch.empty((M, N), dtype=dtype, device=like.device)
+
+
+def _int8_rows(M: int, K: int, like: torch.Tensor):
     """int8 [M][K] whose row stride is a multiple of 16, as the products need it."""
     ld = -(-K // 16) * 16
-    q = torch.empty((M, ld), dtype=torch.int8, device=device)
-    return q if ld == K else q[:, :K]
+    q = _matrix(M, ld, torch.int8, like)
+    return (q if ld == K else q[:, :K]), ld
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -435,20 +448,23 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     ldx = _rows(x, "x", _FLOATING)
     M, D = x.shape
     w, b, wt = _affine(weight, bias, D)
-    if out is not None and out_dtype not in (None, out.dtype):
-        raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    s, ctx = _where(stream, x, weight, bias, out)
-    with ctx:
-        if out is None:
-            out = torch.empty((M, D), dtype=out_dtype or x.dtype, device=x.device)
+    if out is not None:
+        if out_dtype not in (None, out.dtype):
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
         ldy = _rows(out, "out", _FLOATING, (M, D))
-        mean = rstd = None
-        if stats:
-            mean = torch.empty(M, dtype=torch.float32, device=x.device)
-            rstd = torch.empty(M, dtype=torch.float32, device=x.device)
-        _check(lib().twell_layer_norm_fwd(x.data_ptr(), _DTYPES[x.dtype], ldx, w, b, wt, M, D, eps, out.data_ptr(),
-                                          _DTYPES[out.dtype], ldy, mean.data_ptr() if stats else None,
-                                          rstd.data_ptr() if stats else None, s), "twell_layer_norm_fwd")
+    elif out_dtype is not None and out_dtype not in _FLOATING:
+        raise ValueError(f"out_dtype must be one of {_FLOATING}, got {out_dtype}")
+    if _elsewhere(stream, x, weight, bias, out):
+        with _there(stream, x):
+            return layer_norm(x, weight, bias, eps, out, out_dtype, stats)
+    if out is None:
+        out, ldy = _matrix(M, D, out_dtype or x.dtype, x), D
+    mean = rstd = pm = pr = None
+    if stats:
+        mean, rstd = _matrix(2, M, torch.float32, x).unbind()
+        pm, pr = mean.data_ptr(), rstd.data_ptr()
+    _check(lib().twell_layer_norm_fwd(x.data_ptr(), _DTYPES[x.dtype], ldx, w, b, wt, M, D, eps, out.data_ptr(),
+                                      _DTYPES[out.dtype], ldy, pm, pr, _here(x)), "twell_layer_norm_fwd")
     return (out, mean, rstd) if stats else out
 
 
@@ -459,12 +475,13 @@ def layer_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias
     ldx = _rows(x, "x", _FLOATING)
     M, D = x.shape
     w, b, wt = _affine(weight, bias, D)
-    s, ctx = _where(stream, x, weight, bias)
-    with ctx:
-        q = _int8_rows(M, D, x.device)
-        scale = torch.empty(M, dtype=torch.float32, device=x.device)
-        _check(lib().twell_layer_norm_int8(x.data_ptr(), _DTYPES[x.dtype], ldx, w, b, wt, M, D, eps, q.data_ptr(),
-                                           q.stride(0), scale.data_ptr(), None, None, s), "twell_layer_norm_int8")
+    if _elsewhere(stream, x, weight, bias):
+        with _there(stream, x):
+            return layer_norm_int8(x, weight, bias, eps)
+    q, ldq = _int8_rows(M, D, x)
+    scale = torch.empty(M, dtype=torch.float32, device=x.device)
+    _check(lib().twell_layer_norm_int8(x.data_ptr(), _DTYPES[x.dtype], ldx, w, b, wt, M, D, eps, q.data_ptr(), ldq,
+                                       scale.data_ptr(), None, None, _here(x)), "twell_layer_norm_int8")
     return q, scale
 
 
@@ -479,28 +496,28 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: 
     M, D = x.shape
     lddy = _rows(dy, "dy", _FLOATING, (M, D))
     w = _vector(weight, "weight", D, _FLOATING)
-    s, ctx = _where(stream, x, dy, mean, rstd, weight, scratch)
+    pm, pr = _vector(mean, "mean", M), _vector(rstd, "rstd", M)
+    if scratch is not None and not scratch.is_contiguous():
+        raise ValueError("scratch must be contiguous")
+    if _elsewhere(stream, x, dy, mean, rstd, weight, scratch):
+        with _there(stream, x):
+            return layer_norm_bwd(dy, x, mean, rstd, weight, param_grads, scratch)
     L = lib()
-    with ctx:
-        dx = torch.empty((M, D), dtype=x.dtype, device=x.device)
-        dw = db = None
-        need = 0
-        if param_grads:
-            dw = torch.empty(D, dtype=torch.float32, device=x.device)
-            db = torch.empty(D, dtype=torch.float32, device=x.device)
-            need = L.twell_layer_norm_bwd_scratch_bytes(M, D)
-            if scratch is None:
-                scratch = torch.empty(need, dtype=torch.uint8, device=x.device)
-            elif not scratch.is_contiguous():
-                raise ValueError("scratch must be contiguous")
-        _check(L.twell_layer_norm_bwd(dy.data_ptr(), _DTYPES[dy.dtype], lddy, x.data_ptr(), _DTYPES[x.dtype], ldx,
-                                      _vector(mean, "mean", M), _vector(rstd, "rstd", M), w,
-                                      0 if weight is None else _DTYPES[weight.dtype], M, D, dx.data_ptr(),
-                                      _rows(dx, "dx", _FLOATING), dw.data_ptr() if param_grads else None,
-                                      db.data_ptr() if param_grads else None,
-                                      scratch.data_ptr() if param_grads else None,
-                                      scratch.numel() * scratch.element_size() if param_grads else 0, s),
-               "twell_layer_norm_bwd")
+    dx = _matrix(M, D, x.dtype, x)
+    dw = db = pw = pb = ps = None
+    size = 0
+    if param_grads:
+        dw, db = _matrix(2, D, torch.float32, x).unbind()
+        pw, pb = dw.data_ptr(), db.data_ptr()
+        if scratch is None:
+            size = L.twell_layer_norm_bwd_scratch_bytes(M, D)
+            scratch = torch.empty(size, dtype=torch.uint8, device=x.device)
+        else:
+            size = scratch.numel() * scratch.element_size()
+        ps = scratch.data_ptr()
+    _check(L.twell_layer_norm_bwd(dy.data_ptr(), _DTYPES[dy.dtype], lddy, x.data_ptr(), _DTYPES[x.dtype], ldx, pm, pr, w,
+                                  0 if weight is None else _DTYPES[weight.dtype], M, D, dx.data_ptr(), D, pw, pb, ps,
+                                  size, _here(x)), "twell_layer_norm_bwd")
     return dx, dw, db
 
 
@@ -509,12 +526,13 @@ def quantize_rows(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Ten
     activations (a scale per token) and weights [N][K] (one per channel)."""
     ldx = _rows(x, "x", _FLOATING)
     M, K = x.shape
-    s, ctx = _where(stream, x)
-    with ctx:
-        q = _int8_rows(M, K, x.device)
-        scale = torch.empty(M, dtype=torch.float32, device=x.device)
-        _check(lib().twell_quantize_rows(x.data_ptr(), _DTYPES[x.dtype], ldx, M, K, q.data_ptr(), q.stride(0),
-                                         scale.data_ptr(), s), "twell_quantize_rows")
+    if _elsewhere(stream, x):
+        with _there(stream, x):
+            return quantize_rows(x)
+    q, ldq = _int8_rows(M, K, x)
+    scale = torch.empty(M, dtype=torch.float32, device=x.device)
+    _check(lib().twell_quantize_rows(x.data_ptr(), _DTYPES[x.dtype], ldx, M, K, q.data_ptr(), ldq, scale.data_ptr(),
+                                     _here(x)), "twell_quantize_rows")
     return q, scale
 
 
@@ -523,14 +541,33 @@ def dequantize_rows(q: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dtype
     """twell_dequantize_rows: q scale, of out_dtype."""
     ldq = _rows(q, "q", _I8)
     M, K = q.shape
+    ps = _vector(scale, "scale", M)
     if out_dtype not in _FLOATING:
         raise ValueError(f"out_dtype must be one of {_FLOATING}, got {out_dtype}")
-    s, ctx = _where(stream, q, scale)
-    with ctx:
-        y = torch.empty((M, K), dtype=out_dtype, device=q.device)
-        _check(lib().twell_dequantize_rows(q.data_ptr(), ldq, _vector(scale, "scale", M), M, K, y.data_ptr(),
-                                           _DTYPES[out_dtype], K, s), "twell_dequantize_rows")
+    if _elsewhere(stream, q, scale):
+        with _there(stream, q):
+            return dequantize_rows(q, scale, out_dtype)
+    y = _matrix(M, K, out_dtype, q)
+    _check(lib().twell_dequantize_rows(q.data_ptr(), ldq, ps, M, K, y.data_ptr(), _DTYPES[out_dtype], K, _here(q)),
+           "twell_dequantize_rows")
     return y
+
+
+def _product_rows(x, w, name):
+    """Row strides and sizes of a product's int8 operands."""
+    ldx, ldw = _rows(x, "x", _I8), _rows(w, name, _I8)
+    (M, K), (N, Kw) = x.shape, w.shape
+    if Kw != K:
+        raise ValueError(f"x {tuple(x.shape)} and {name} {tuple(w.shape)} must have rows of one length")
+    return ldx, ldw, M, N, K
+
+
+def _product_out(out, out_dtype, M, N):
+    if out is not None:
+        return _rows(out, "out", _FLOATING, (M, N))
+    if out_dtype not in _FLOATING:
+        raise ValueError(f"out_dtype must be one of {_FLOATING}, got {out_dtype}")
+    return N
 
 
 def int8_linear(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -539,19 +576,15 @@ def int8_linear(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     """twell_int8_linear: y [M][N] = x w^T x_scale w_scale (+ bias) from int8
     rows x [M][K] and w [N][K] (bases 16-byte aligned, row strides multiples of
     16, as quantize_rows makes them)."""
-    ldx, ldw = _rows(x, "x", _I8), _rows(w, "w", _I8)
-    (M, K), N = x.shape, w.shape[0]
-    if w.shape[1] != K:
-        raise ValueError(f"x {tuple(x.shape)} and w {tuple(w.shape)} must have rows of one length")
-    if out is None and out_dtype not in _FLOATING:
-        raise ValueError(f"out_dtype must be one of {_FLOATING}, got {out_dtype}")
-    s, ctx = _where(stream, x, x_scale, w, w_scale, bias, out)
-    with ctx:
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device) if out is None else out
-        _check(lib().twell_int8_linear(x.data_ptr(), ldx, _vector(x_scale, "x_scale", M), w.data_ptr(), ldw,
-                                       _vector(w_scale, "w_scale", N), _vector(bias, "bias", N), M, N, K, y.data_ptr(),
-                                       _DTYPES.get(y.dtype, -1), _rows(y, "out", _FLOATING, (M, N)), s),
-               "twell_int8_linear")
+    ldx, ldw, M, N, K = _product_rows(x, w, "w")
+    ldy = _product_out(out, out_dtype, M, N)
+    xs, ws, pb = _vector(x_scale, "x_scale", M), _vector(w_scale, "w_scale", N), _vector(bias, "bias", N)
+    if _elsewhere(stream, x, x_scale, w, w_scale, bias, out):
+        with _there(stream, x):
+            return int8_linear(x, x_scale, w, w_scale, bias, out_dtype, out)
+    y = _matrix(M, N, out_dtype, x) if out is None else out
+    _check(lib().twell_int8_linear(x.data_ptr(), ldx, xs, w.data_ptr(), ldw, ws, pb, M, N, K, y.data_ptr(),
+                                   _DTYPES[y.dtype], ldy, _here(x)), "twell_int8_linear")
     return y
 
 
@@ -560,21 +593,16 @@ def int8_gated(x: torch.Tensor, x_scale: torch.Tensor, wg: torch.Tensor, wg_scal
                stream=None) -> torch.Tensor:
     """twell_int8_gated: h [M][N] = u ReLU(g) with g, u the int8 products of x
     with wg and wu (operands as for int8_linear)."""
-    ldx, ldg = _rows(x, "x", _I8), _rows(wg, "wg", _I8)
-    (M, K), N = x.shape, wg.shape[0]
-    if wg.shape[1] != K:
-        raise ValueError(f"x {tuple(x.shape)} and wg {tuple(wg.shape)} must have rows of one length")
+    ldx, ldg, M, N, K = _product_rows(x, wg, "wg")
     ldu = _rows(wu, "wu", _I8, (N, K))
-    if out is None and out_dtype not in _FLOATING:
-        raise ValueError(f"out_dtype must be one of {_FLOATING}, got {out_dtype}")
-    s, ctx = _where(stream, x, x_scale, wg, wg_scale, wu, wu_scale, out)
-    with ctx:
-        h = torch.empty((M, N), dtype=out_dtype, device=x.device) if out is None else out
-        _check(lib().twell_int8_gated(x.data_ptr(), ldx, _vector(x_scale, "x_scale", M), wg.data_ptr(), ldg,
-                                      _vector(wg_scale, "wg_scale", N), wu.data_ptr(), ldu,
-                                      _vector(wu_scale, "wu_scale", N), M, N, K, h.data_ptr(),
-                                      _DTYPES.get(h.dtype, -1), _rows(h, "out", _FLOATING, (M, N)), s),
-               "twell_int8_gated")
+    ldh = _product_out(out, out_dtype, M, N)
+    xs, gs, us = _vector(x_scale, "x_scale", M), _vector(wg_scale, "wg_scale", N), _vector(wu_scale, "wu_scale", N)
+    if _elsewhere(stream, x, x_scale, wg, wg_scale, wu, wu_scale, out):
+        with _there(stream, x):
+            return int8_gated(x, x_scale, wg, wg_scale, wu, wu_scale, out_dtype, out)
+    h = _matrix(M, N, out_dtype, x) if out is None else out
+    _check(lib().twell_int8_gated(x.data_ptr(), ldx, xs, wg.data_ptr(), ldg, gs, wu.data_ptr(), ldu, us, M, N, K,
+                                  h.data_ptr(), _DTYPES[h.dtype], ldh, _here(x)), "twell_int8_gated")
     return h
 
 
