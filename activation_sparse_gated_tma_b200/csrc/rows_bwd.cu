@@ -1,8 +1,12 @@
 // Layer norm's backward pass: launches and type dispatch (kernels in rows.cuh).
+#include "rows_bwd.cuh"
 #include "rows_launch.h"
 
 namespace twell {
 namespace {
+
+constexpr int64_t kSmShared = 220 * 1024;  // of an SM's 227 KB, for the dynamic shared memory of its blocks
+constexpr int64_t kBlockFixed = 3 * 1024;  // of a block besides: static and reserved
 
 // Sums `parts` partial rows of 2 D values: a block takes 32 columns with 16
 // warps, each adding every 16th row, then the warps' sums in a fixed order.
@@ -97,7 +101,9 @@ int layer_norm_bwd_max_parts(int M, int D, int sms) {
 }
 
 cudaError_t launch_layer_norm_bwd(const LayerNormBwdParams& p, int sms, int& parts, cudaStream_t s) {
-  const bool vec = p.D % 4 == 0 && quads(p.x, p.ldx, p.x_type) && quads(p.dx, p.lddx, p.x_type) && quads(p.dy, p.lddy, p.dy_type);
+  const bool vec = p.D % 4 == 0 && aligned_rows(p.x, p.ldx * type_size(p.x_type), 16) &&
+                   aligned_rows(p.dx, p.lddx * type_size(p.x_type), 16) &&
+                   aligned_rows(p.dy, p.lddy * type_size(p.dy_type), 16);
   if (p.x_type == TWELL_F32) {
     if (p.dy_type == TWELL_F32) return norm_bwd<float, float>(p, vec, sms, parts, s);
     if (p.dy_type == TWELL_BF16) return norm_bwd<float, bf16>(p, vec, sms, parts, s);

@@ -5,26 +5,26 @@ namespace twell {
 namespace {
 
 template <class TI>
-cudaError_t quantize(const QuantizeParams& p, bool vec, int sms, cudaStream_t s) {
+cudaError_t quantize(const QuantizeParams& p, bool aligned, int sms, cudaStream_t s) {
   if (p.K > kQuantizeMaxRow)
     return launch_pdl(quantize_long_rows_kernel<TI>, p.M < 4 * sms ? p.M : 4 * sms, kRowThreads, 0, s, p);
-  const RowShape r = row_shape(p.M, p.K, sms);
-  uint32_t begin = 0, end = p.M;
-  rows_inside(p.x, p.ldx, p.M, p.K, p.type, begin, end);
+  const RowShape r = row_shape(p.M, p.K, kQuantizeChunks, sms);
+  RowPlan plan{r.warps, 0, static_cast<uint32_t>(p.M)};
+  rows_inside(p.x, p.ldx, p.M, p.K, p.type, plan.begin, plan.end);
   void (*kern)(const QuantizeParams, const RowPlan) = nullptr;
-#define TW_NG(n) \
+#define TW_NC(n) \
   case n:        \
-    kern = vec ? quantize_rows_kernel<TI, n, true> : quantize_rows_kernel<TI, n, false>; \
+    kern = aligned ? quantize_rows_kernel<TI, n, true> : quantize_rows_kernel<TI, n, false>; \
     break;
-  switch (r.layers) { TW_NG(1) TW_NG(2) TW_NG(4) TW_NG(8) TW_NG(12) TW_NG(16) TW_NG(20) }
-#undef TW_NG
-  return launch_rows(kern, p, r, row_slot_bytes(p.K * sizeof(TI)), 0, begin, end, sms, s);
+  switch (r.chunks) { TW_NC(1) TW_NC(2) TW_NC(3) TW_NC(4) TW_NC(5) TW_NC(6) TW_NC(8) TW_NC(10) }
+#undef TW_NC
+  return launch_pdl(kern, row_grid(p.M, r, quantize_blocks(r.chunks, sizeof(TI)), sms), r.threads(), 0, s, p, plan);
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_rows(const QuantizeParams& p, int sms, cudaStream_t s) {
-  const bool vec = p.K % 4 == 0 && quads(p.x, p.ldx, p.type) && quads(p.y, p.ldy, TWELL_I8);
+  const bool vec = p.K % 8 == 0 && aligned_rows(p.x, p.ldx * type_size(p.type), 16) && aligned_rows(p.y, p.ldy, 8);
   if (p.type == TWELL_F32) return quantize<float>(p, vec, sms, s);
   if (p.type == TWELL_BF16) return quantize<bf16>(p, vec, sms, s);
   return quantize<__half>(p, vec, sms, s);
@@ -32,12 +32,13 @@ cudaError_t launch_quantize_rows(const QuantizeParams& p, int sms, cudaStream_t 
 
 template <class TO>
 static cudaError_t dequantize(const QuantizeParams& p, int sms, cudaStream_t s) {
-  const bool q_aligned = quads(p.x, p.ldx, TWELL_I8), vec = p.K % 4 == 0 && quads(p.y, p.ldy, p.type);
+  const bool q_aligned = aligned_rows(p.x, p.ldx, 8);
+  const bool vec = p.K % 8 == 0 && aligned_rows(p.y, p.ldy * type_size(p.type), 16);
   int across = 32;
-  while (across < 256 && across * 16 < p.K) across *= 2;
+  while (across < 256 && across * 32 < p.K) across *= 2;  // four chunks a thread
   const int high = 256 / across;
   const int64_t need = (static_cast<int64_t>(p.M) + high - 1) / high;
-  const int grid = static_cast<int>(need < 8 * sms ? need : 8 * sms);
+  const int grid = static_cast<int>(need < 64 * sms ? need : 64 * sms);
   auto kern = q_aligned ? (vec ? dequantize_rows_kernel<TO, true, true> : dequantize_rows_kernel<TO, true, false>)
                         : (vec ? dequantize_rows_kernel<TO, false, true> : dequantize_rows_kernel<TO, false, false>);
   return launch_pdl(kern, grid, 256, 0, s, p, across);

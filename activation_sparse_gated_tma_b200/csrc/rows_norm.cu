@@ -5,25 +5,31 @@ namespace twell {
 namespace {
 
 template <class TI, class TO>
-cudaError_t norm(const LayerNormParams& p, bool vec, int sms, cudaStream_t s) {
-  const RowShape r = row_shape(p.M, p.D, sms);
-  uint32_t begin = 0, end = p.M;
-  rows_inside(p.x, p.ldx, p.M, p.D, p.x_type, begin, end);
+cudaError_t norm(const LayerNormParams& p, bool aligned, int sms, cudaStream_t s) {
+  const RowShape r = row_shape(p.M, p.D, aligned ? kNormChunks : kNormChunksUnaligned, sms);
+  RowPlan plan{r.warps, 0, static_cast<uint32_t>(p.M)};
+  rows_inside(p.x, p.ldx, p.M, p.D, p.x_type, plan.begin, plan.end);
   void (*kern)(const LayerNormParams, const RowPlan) = nullptr;
-#define TW_NG(n) \
+#define TW_NC(n) \
   case n:        \
-    kern = vec ? layer_norm_kernel<TI, TO, n, true> : layer_norm_kernel<TI, TO, n, false>; \
+    kern = aligned ? layer_norm_kernel<TI, TO, n, true> : layer_norm_kernel<TI, TO, n, false>; \
     break;
-  switch (r.layers) { TW_NG(1) TW_NG(2) TW_NG(4) TW_NG(8) TW_NG(12) TW_NG(16) TW_NG(20) }
-#undef TW_NG
-  return launch_rows(kern, p, r, row_slot_bytes(p.D * sizeof(TI)),
-                     2 * 4 * 4 * r.layers * 32 * r.warps, begin, end, sms, s);
+  switch (r.chunks) { TW_NC(1) TW_NC(2) TW_NC(3) TW_NC(4) TW_NC(5) TW_NC(6) TW_NC(8) TW_NC(10) }
+#undef TW_NC
+  // Weight and bias, 227 KB at most per SM.
+  const int vectors = 2 * 4 * 8 * r.chunks * 32 * r.warps;
+  int per_sm = norm_blocks(r.chunks);
+  while (per_sm > 1 && per_sm * (kRowThreads / r.threads()) * (vectors + 2048) > 220 * 1024) --per_sm;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, vectors);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, row_grid(p.M, r, per_sm, sms), r.threads(), vectors, s, p, plan);
 }
 
 }  // namespace
 
 cudaError_t launch_layer_norm(const LayerNormParams& p, int sms, cudaStream_t s) {
-  const bool vec = p.D % 4 == 0 && quads(p.x, p.ldx, p.x_type) && quads(p.y, p.ldy, p.y_type);
+  const bool vec = p.D % 8 == 0 && aligned_rows(p.x, p.ldx * type_size(p.x_type), 16) &&
+                   aligned_rows(p.y, p.ldy * type_size(p.y_type), p.y_type == TWELL_I8 ? 8 : 16);
   if (p.y_type == TWELL_I8) {
     if (p.x_type == TWELL_F32) return norm<float, int8_t>(p, vec, sms, s);
     if (p.x_type == TWELL_BF16) return norm<bf16, int8_t>(p, vec, sms, s);
