@@ -226,6 +226,14 @@ __device__ __forceinline__ void store_chunk(T* row, uint32_t past, int c, int D,
   }
 }
 
+// Keeps the compiler from carrying a chunk's unpacked elements from one pass
+// over a row to the next: unpacking again costs an instruction per element,
+// holding both forms costs the registers of a third or fourth block per SM.
+template <class T>
+__device__ __forceinline__ void forget_unpacked(Chunk<T>& c) {
+  if constexpr (sizeof(T) == 2) asm volatile("" : "+r"(c.p[0].x), "+r"(c.p[0].y), "+r"(c.p[0].z), "+r"(c.p[0].w));
+}
+
 // ---------------------------------------------------------------- a thread's part of a row
 // NC chunks, the smallest of 1, 2, 3, 4, 5, 6, 8, 10 that covers the row, so
 // that many of the layers are full.
@@ -253,6 +261,16 @@ __device__ __forceinline__ void store_layer(T* row, uint32_t past, int D, int t,
     store_chunk<T, ALIGNED, true>(row, past, 8 * (t + j * nt), D, v);
   else
     store_chunk<T, ALIGNED, false>(row, past, 8 * (t + j * nt), D, v);
+}
+
+// Asks for a row in L2, one thread for the whole row, ahead of its loads (rows
+// whose aligned pieces lie inside the matrix only): the loads then wait for L2
+// instead of DRAM, at no cost in registers.
+template <class T>
+__device__ __forceinline__ void prefetch_row(const T* row, int D) {
+  const uint64_t a = reinterpret_cast<uint64_t>(row), at = a & ~uint64_t(15);
+  const uint32_t bytes = (static_cast<uint32_t>(a - at) + D * static_cast<uint32_t>(sizeof(T)) + 15u) & ~15u;
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
 }
 
 // A parameter vector of D elements into `padded` floats of shared memory, by
@@ -327,9 +345,9 @@ __device__ __forceinline__ float group_max(Group& g, float magnitude) {
 // so the true quotient lies between x low and x high, low and high 2^-22 below
 // and above inv.  Adding 1.5 * 2^23 rounds both to integers (held in the sum's
 // low byte); where they agree that is the answer, else the sign of
-// 254 x - (2 q + 1) amax, exact in 64 bits, decides between q and q + 1.  Rows
-// whose 127 / amax would overflow are scaled up by 2^100 first.  A row with a
-// NaN or an infinity gets scale NaN and q = 0, one of zeros scale 0.
+// 254 x - (2 q + 1) amax decides between q and q + 1.  Rows near either end of
+// the exponents' range are scaled by 2^100 or 2^-100 first.  A row with a NaN or
+// an infinity gets scale NaN and q = 0, one of zeros scale 0.
 struct RowScale {
   float amax, low, high, scale, up;
   bool none;
@@ -339,7 +357,7 @@ __device__ __forceinline__ RowScale row_scale(float amax) {
   const bool finite = amax <= 3.402823466e38f;  // a NaN is not
   r.scale = finite ? amax / 127.f : __uint_as_float(0x7fc00000u);
   r.none = !finite || amax == 0.f;
-  r.up = amax < 0x1p-100f ? 0x1p100f : 1.f;
+  r.up = amax < 0x1p-100f ? 0x1p100f : amax > 0x1p100f ? 0x1p-100f : 1.f;
   r.amax = amax * r.up;
   const float inv = 127.f / r.amax;
   r.low = inv * (1.f - 0x1p-22f);
@@ -349,10 +367,15 @@ __device__ __forceinline__ RowScale row_scale(float amax) {
 __device__ __forceinline__ uint32_t pack_low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
+// t = 254 x - (2 q + 1) amax from the products' roundings and what those leave
+// (Dekker's two-product by fused multiply-add): near a tie the two products are
+// neighbours, so their difference is exact, and a non-zero t is at least 2^-33 of them.
 __device__ __forceinline__ uint32_t nearest(float x, uint32_t a, uint32_t b, float amax) {
   const int q = min(static_cast<int>(a), static_cast<int>(b)) - 0x4b400000;
-  const double t = fma(-static_cast<double>(2 * q + 1), static_cast<double>(amax), 254.0 * static_cast<double>(x));
-  return static_cast<uint32_t>(q + (a != b && (t > 0.0 || (t == 0.0 && (q & 1))) ? 1 : 0));
+  const float k = static_cast<float>(2 * q + 1);
+  const float px = 254.f * x, pa = k * amax;
+  const float t = (px - pa) + (fmaf(254.f, x, -px) - fmaf(k, amax, -pa));
+  return static_cast<uint32_t>(q + (a != b && (t > 0.f || (t == 0.f && (q & 1))) ? 1 : 0));
 }
 // Eight values to eight bytes.
 __device__ __forceinline__ uint2 quantize8(Oct v, const RowScale& r) {
@@ -433,6 +456,9 @@ __global__ void __launch_bounds__(kRowThreads, norm_blocks(NC))
     {
       RowPart<TI, NC> raw;
       load_row<TI, NC, ALIGNED>(static_cast<const TI*>(p.x) + row * p.ldx, plan.whole_pieces(row), p.D, g.t, g.nt, raw);
+      // (Rows of many chunks keep enough loads in flight by themselves: 16384 x 2560 took 39 us with it, 36 without.)
+      if ((!ALIGNED || NC <= 2) && g.t == 0 && plan.whole_pieces(row + step))
+        prefetch_row(static_cast<const TI*>(p.x) + (row + step) * p.ldx, p.D);
 #pragma unroll
       for (int j = 0; j < NC; ++j) v[j] = unpack8(raw.c[j]);
     }
@@ -501,10 +527,14 @@ __global__ void __launch_bounds__(kRowThreads, quantize_blocks(NC, sizeof(TI)))
   for (uint32_t row = blockIdx.x * groups + g.id; row < p.M; row += step) {
     RowPart<TI, NC> v;
     load_row<TI, NC, ALIGNED>(static_cast<const TI*>(p.x) + row * p.ldx, plan.whole_pieces(row), p.K, g.t, g.nt, v);
+    if ((!ALIGNED || NC <= 2) && g.t == 0 && plan.whole_pieces(row + step))
+      prefetch_row(static_cast<const TI*>(p.x) + (row + step) * p.ldx, p.K);
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) m = max_abs(m, unpack8(v.c[j]));
     const RowScale r = row_scale(group_max(g, m));
+#pragma unroll
+    for (int j = 0; j < NC; ++j) forget_unpacked(v.c[j]);
     store_row_i8<NC, ALIGNED>(static_cast<int8_t*>(p.y) + row * p.ldy, p.K, g.t, g.nt, r,
                               [&](int j) { return unpack8(v.c[j]); });
     if (g.t == 0) p.scale[row] = r.scale;
@@ -558,7 +588,7 @@ __global__ void __launch_bounds__(256) dequantize_rows_kernel(const QuantizePara
   griddep_wait();
   const int tx = static_cast<int>(threadIdx.x) % across, ty = static_cast<int>(threadIdx.x) / across;
   const int high = 256 / across;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 3;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * high + ty; row < p.M; row += static_cast<int64_t>(gridDim.x) * high) {
     const int8_t* q = static_cast<const int8_t*>(p.x) + row * p.ldx;
     TO* y = static_cast<TO*>(p.y) + row * p.ldy;

@@ -7,25 +7,21 @@
 
 namespace twell {
 
-// Shared memory of one row in a ring slot (backward): its bytes, up to 15 before
-// them, the rest of the last 16 and what a shifted read takes behind it.
-__host__ __device__ constexpr uint32_t row_slot_bytes(uint32_t row_bytes) { return (row_bytes + 46) / 16 * 16; }
-
 constexpr int kRowThreads = 256;     // of a block at most
 constexpr int kMaxGroups = 8;        // rows that a block works on at once
 constexpr int kMaxGroupWarps = 8;    // of a row
 constexpr int kNormChunks = 10;      // of eight elements that a thread holds at most
 constexpr int kNormChunksUnaligned = 6;  // joining pieces wants more warps (bf16, 8191 x 4095: 80 us with 10, 62 with 6)
 constexpr int kQuantizeChunks = 6;   // as long as kMaxGroupWarps warps hold the row so
-constexpr int kMaxSlots = 4;         // of a ring
-constexpr int kMaxBatch = 8;         // rows of a batch, backward
 constexpr int kBwdThreads = 512;     // of a block at most, backward
 constexpr int kLayerNormMaxD = 16384;
 constexpr int kQuantizeMaxRow = 8 * kNormChunks * kRowThreads;  // longer rows are read twice
 
 // Blocks that share an SM's registers.
 constexpr int norm_blocks(int chunks) { return chunks <= 2 ? 4 : chunks <= 5 ? 3 : 2; }
-constexpr int quantize_blocks(int chunks, int element) { return chunks * element <= 8 ? 4 : chunks * element <= 12 ? 3 : 2; }
+constexpr int quantize_blocks(int chunks, int element) { return chunks * element <= 12 ? 4 : chunks * element <= 20 ? 3 : 2; }
+
+constexpr int bwd_registers(int chunks) { return chunks == 1 ? 80 : 128; }
 
 // How a launch lays out rows over blocks (see rows.cuh): warps per row; rows
 // [begin, end) are those whose aligned pieces lie inside the matrix.
@@ -34,12 +30,7 @@ struct RowPlan {
   uint32_t begin, end;
   __host__ __device__ bool whole_pieces(uint32_t row) const { return row >= begin && row < end; }
 };
-// Backward: rows of a batch, ring slots, batches; rows [ring_begin, ring_end)
-// pass through the ring (their 16-byte pieces lie inside the matrices).
-struct BatchPlan {
-  int rows, slots;
-  uint32_t batches, ring_begin, ring_end;
-};
+using BwdPlan = RowPlan;
 
 // Rows are `ld` elements apart; a row's elements are contiguous.  Types are
 // twell_dtype values; out_type TWELL_I8 writes quantised rows and y_scale.
@@ -73,10 +64,9 @@ struct LayerNormBwdParams {
   float inv_d;         // 1 / D
   int dy_type, x_type, w_type;
 };
-// Most partial rows of the parameter gradients that a call writes.
-int layer_norm_bwd_max_parts(int M, int D, int sms);
-// Returns the partial rows it writes in `parts`.
-cudaError_t launch_layer_norm_bwd(const LayerNormBwdParams& p, int sms, int& parts, cudaStream_t s);
+// Partial rows of the parameter gradients that a call writes.
+int layer_norm_bwd_parts(int M, int D, int sms);
+cudaError_t launch_layer_norm_bwd(const LayerNormBwdParams& p, int sms, cudaStream_t s);
 cudaError_t launch_layer_norm_bwd_reduce(const LayerNormBwdParams& p, int parts, cudaStream_t s);
 
 struct QuantizeParams {

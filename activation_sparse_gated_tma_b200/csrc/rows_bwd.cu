@@ -1,12 +1,9 @@
-// Layer norm's backward pass: launches and type dispatch (kernels in rows.cuh).
+// Layer norm's backward pass: launches and type dispatch (kernels in rows_bwd.cuh).
 #include "rows_bwd.cuh"
 #include "rows_launch.h"
 
 namespace twell {
 namespace {
-
-constexpr int64_t kSmShared = 220 * 1024;  // of an SM's 227 KB, for the dynamic shared memory of its blocks
-constexpr int64_t kBlockFixed = 3 * 1024;  // of a block besides: static and reserved
 
 // Sums `parts` partial rows of 2 D values: a block takes 32 columns with 16
 // warps, each adding every 16th row, then the warps' sums in a fixed order.
@@ -20,6 +17,7 @@ __global__ void __launch_bounds__(32 * kReduceWarps)
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.f;
   if (c < 2 * static_cast<int64_t>(D))
+#pragma unroll 8
     for (int r = warp; r < parts; r += kReduceWarps) s += partial[static_cast<int64_t>(r) * 2 * D + c];
   sums[warp][lane] = s;
   __syncthreads();
@@ -35,85 +33,59 @@ __global__ void __launch_bounds__(32 * kReduceWarps)
   }
 }
 
-// Layers of four columns a thread owns: the fewest of 2, 4, 8 with which kBwdThreads threads own a row.
-int bwd_layers(int D) { return D <= 8 * kBwdThreads ? 2 : D <= 16 * kBwdThreads ? 4 : 8; }
-int bwd_threads(int D) {
-  const int span = 128 * bwd_layers(D);
-  return (D + span - 1) / span * 32;
-}
-int bwd_blocks(int D) {
-  const int threads = bwd_layers(D) == 2 ? 1024 : 512;  // what the registers allow an SM
-  const int blocks = threads / bwd_threads(D);
-  return blocks < 1 ? 1 : blocks > 8 ? 8 : blocks;
+// Chunks a thread owns: the fewest of 1, 2, 4 with which kBwdThreads threads
+// own a row; two rows at a time where one chunk leaves the registers for it.
+struct BwdShape {
+  int chunks, warps, groups, rows, grid;
+};
+BwdShape bwd_shape(int M, int D, int sms) {
+  BwdShape r;
+  r.chunks = D <= 8 * kBwdThreads ? 1 : D <= 16 * kBwdThreads ? 2 : 4;
+  r.rows = r.chunks == 1 ? 2 : 1;
+  r.warps = (D + 256 * r.chunks - 1) / (256 * r.chunks);
+  r.groups = r.warps < kMaxGroups ? kMaxGroups / r.warps : 1;
+  const int64_t each = (static_cast<int64_t>(M) + static_cast<int64_t>(sms) * r.rows - 1) / (static_cast<int64_t>(sms) * r.rows);
+  if (r.groups > each) r.groups = static_cast<int>(each);
+  const int threads = 32 * r.warps * r.groups;
+  const int resident = 65536 / bwd_registers(r.chunks);
+  const int per_sm = resident / threads > 1 ? resident / threads : 1;
+  const int64_t need = (static_cast<int64_t>(M) + r.groups * r.rows - 1) / (r.groups * r.rows);
+  const int64_t most = static_cast<int64_t>(sms) * per_sm;
+  r.grid = static_cast<int>(need < most ? need : most);
+  return r;
 }
 
 template <class TX, class TDY>
-cudaError_t norm_bwd(const LayerNormBwdParams& p, bool vec, int sms, int& parts, cudaStream_t s) {
-  const int layers = bwd_layers(p.D), threads = bwd_threads(p.D), warps = threads / 32;
-  const int64_t row = row_slot_bytes(p.D * sizeof(TX)) + row_slot_bytes(p.D * sizeof(TDY));
-  const int64_t vector = 4 * 4 * layers * threads;
-  // Blocks per SM and rows per batch: the most blocks with which two batches
-  // of two rows fit (else one block), batches as large as two of them fit.
-  int per_sm = bwd_blocks(p.D);
-  auto room = [&](int n) { return kSmShared / n - kBlockFixed - vector; };
-  while (per_sm > 1 && room(per_sm) < 4 * row) --per_sm;
-  int rows = static_cast<int>(room(per_sm) / (2 * row));
-  if (rows > kMaxBatch) rows = kMaxBatch;
-  // Few rows: batches small enough to occupy every block.
-  const int64_t spread = (static_cast<int64_t>(p.M) + static_cast<int64_t>(sms) * per_sm - 1) / (static_cast<int64_t>(sms) * per_sm);
-  if (rows > spread) rows = static_cast<int>(spread);
-  if (rows < 1) rows = 1;
-  // Whole numbers of warps per row, if a slightly smaller batch has one.
-  for (int k = rows; k > rows / 2; --k)
-    if (warps % k == 0) {
-      rows = k;
-      break;
-    }
-  BatchPlan plan;
-  plan.rows = rows;
-  plan.batches = (static_cast<uint32_t>(p.M) + rows - 1) / rows;
-  const int64_t most = static_cast<int64_t>(sms) * per_sm;
-  const int grid = static_cast<int>(plan.batches < most ? plan.batches : most);
-  const int64_t each = (plan.batches + grid - 1) / grid;
-  int64_t slots = room(per_sm) / (rows * row);
-  if (slots > 4) slots = 4;
-  if (slots > each) slots = each;
-  plan.slots = static_cast<int>(slots < 1 ? 1 : slots);
-  plan.ring_begin = 0;
-  plan.ring_end = p.M;
-  rows_inside(p.x, p.ldx, p.M, p.D, p.x_type, plan.ring_begin, plan.ring_end);
-  rows_inside(p.dy, p.lddy, p.M, p.D, p.dy_type, plan.ring_begin, plan.ring_end);
-  const size_t smem = static_cast<size_t>(vector + plan.slots * rows * row);
-  auto kern = layers == 2   ? (vec ? layer_norm_bwd_kernel<TX, TDY, 2, true> : layer_norm_bwd_kernel<TX, TDY, 2, false>)
-              : layers == 4 ? (vec ? layer_norm_bwd_kernel<TX, TDY, 4, true> : layer_norm_bwd_kernel<TX, TDY, 4, false>)
-                            : (vec ? layer_norm_bwd_kernel<TX, TDY, 8, true> : layer_norm_bwd_kernel<TX, TDY, 8, false>);
-  parts = grid;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kern, grid, threads, smem, s, p, plan);
+cudaError_t norm_bwd(const LayerNormBwdParams& p, bool aligned, int sms, cudaStream_t s) {
+  const BwdShape r = bwd_shape(p.M, p.D, sms);
+  BwdPlan plan{r.warps, 0, static_cast<uint32_t>(p.M)};
+  rows_inside(p.x, p.ldx, p.M, p.D, p.x_type, plan.begin, plan.end);
+  rows_inside(p.dy, p.lddy, p.M, p.D, p.dy_type, plan.begin, plan.end);
+  auto kern = r.chunks == 1   ? (aligned ? layer_norm_bwd_kernel<TX, TDY, 1, 2, true> : layer_norm_bwd_kernel<TX, TDY, 1, 2, false>)
+              : r.chunks == 2 ? (aligned ? layer_norm_bwd_kernel<TX, TDY, 2, 1, true> : layer_norm_bwd_kernel<TX, TDY, 2, 1, false>)
+                              : (aligned ? layer_norm_bwd_kernel<TX, TDY, 4, 1, true> : layer_norm_bwd_kernel<TX, TDY, 4, 1, false>);
+  const size_t smem = r.groups > 1 ? static_cast<size_t>(r.groups) * 2 * p.D * sizeof(float) : 0;  // 16 KB at most
+  return launch_pdl(kern, r.grid, 32 * r.warps * r.groups, smem, s, p, plan);
 }
 
 }  // namespace
 
-int layer_norm_bwd_max_parts(int M, int D, int sms) {
-  const int64_t most = static_cast<int64_t>(sms) * bwd_blocks(D);
-  return static_cast<int>(M < most ? M : most);
-}
+int layer_norm_bwd_parts(int M, int D, int sms) { return bwd_shape(M, D, sms).grid; }
 
-cudaError_t launch_layer_norm_bwd(const LayerNormBwdParams& p, int sms, int& parts, cudaStream_t s) {
-  const bool vec = p.D % 4 == 0 && aligned_rows(p.x, p.ldx * type_size(p.x_type), 16) &&
+cudaError_t launch_layer_norm_bwd(const LayerNormBwdParams& p, int sms, cudaStream_t s) {
+  const bool vec = p.D % 8 == 0 && aligned_rows(p.x, p.ldx * type_size(p.x_type), 16) &&
                    aligned_rows(p.dx, p.lddx * type_size(p.x_type), 16) &&
                    aligned_rows(p.dy, p.lddy * type_size(p.dy_type), 16);
   if (p.x_type == TWELL_F32) {
-    if (p.dy_type == TWELL_F32) return norm_bwd<float, float>(p, vec, sms, parts, s);
-    if (p.dy_type == TWELL_BF16) return norm_bwd<float, bf16>(p, vec, sms, parts, s);
-    return norm_bwd<float, __half>(p, vec, sms, parts, s);
+    if (p.dy_type == TWELL_F32) return norm_bwd<float, float>(p, vec, sms, s);
+    if (p.dy_type == TWELL_BF16) return norm_bwd<float, bf16>(p, vec, sms, s);
+    return norm_bwd<float, __half>(p, vec, sms, s);
   }
   if (p.x_type == TWELL_BF16)
-    return p.dy_type == TWELL_F32 ? norm_bwd<bf16, float>(p, vec, sms, parts, s)
-                                  : norm_bwd<bf16, bf16>(p, vec, sms, parts, s);
-  return p.dy_type == TWELL_F32 ? norm_bwd<__half, float>(p, vec, sms, parts, s)
-                                : norm_bwd<__half, __half>(p, vec, sms, parts, s);
+    return p.dy_type == TWELL_F32 ? norm_bwd<bf16, float>(p, vec, sms, s)
+                                  : norm_bwd<bf16, bf16>(p, vec, sms, s);
+  return p.dy_type == TWELL_F32 ? norm_bwd<__half, float>(p, vec, sms, s)
+                                : norm_bwd<__half, __half>(p, vec, sms, s);
 }
 
 cudaError_t launch_layer_norm_bwd_reduce(const LayerNormBwdParams& p, int parts, cudaStream_t s) {

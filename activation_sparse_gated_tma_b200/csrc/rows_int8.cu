@@ -34,8 +34,7 @@ template <class TO>
 static cudaError_t dequantize(const QuantizeParams& p, int sms, cudaStream_t s) {
   const bool q_aligned = aligned_rows(p.x, p.ldx, 8);
   const bool vec = p.K % 8 == 0 && aligned_rows(p.y, p.ldy * type_size(p.type), 16);
-  int across = 32;
-  while (across < 256 && across * 32 < p.K) across *= 2;  // four chunks a thread
+  const int across = p.K > 4096 ? 256 : p.K > 2048 ? 128 : p.K > 1024 ? 64 : 32;  // two to four chunks a thread
   const int high = 256 / across;
   const int64_t need = (static_cast<int64_t>(p.M) + high - 1) / high;
   const int grid = static_cast<int>(need < 64 * sms ? need : 64 * sms);
