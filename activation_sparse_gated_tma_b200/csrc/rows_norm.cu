@@ -20,8 +20,10 @@ cudaError_t norm(const LayerNormParams& p, bool aligned, int sms, cudaStream_t s
   const int vectors = 2 * 4 * 8 * r.chunks * 32 * r.warps;
   int per_sm = norm_blocks(r.chunks);
   while (per_sm > 1 && per_sm * (kRowThreads / r.threads()) * (vectors + 2048) > 220 * 1024) --per_sm;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, vectors);
-  if (e != cudaSuccess) return e;
+  if (vectors > 48 * 1024) {  // else no attribute is needed
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, vectors);
+    if (e != cudaSuccess) return e;
+  }
   return launch_pdl(kern, row_grid(p.M, r, per_sm, sms), r.threads(), vectors, s, p, plan);
 }
 

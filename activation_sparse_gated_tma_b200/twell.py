@@ -375,7 +375,7 @@ def _elsewhere(stream, *tensors) -> bool:
             raise ValueError(f"tensors on {tensors[0].device} and {t.device}")
     if d < 0:
         raise ValueError(f"tensors must be on a CUDA device, not {tensors[0].device}")
-    return stream is not None or d != torch.cuda.current_device()
+    return stream is not None or d != _current_device()
 
 
 def _there(stream, t: torch.Tensor):
@@ -386,6 +386,10 @@ def _there(stream, t: torch.Tensor):
     if stream.device != t.device:
         raise ValueError(f"stream on {stream.device}, tensors on {t.device}")
     return torch.cuda.stream(stream)
+
+
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()  # torch.cuda.current_device() less its lazy initialisation: t is on a device
 
 
 def _here(t: torch.Tensor) -> int:
@@ -427,7 +431,7 @@ def _affine(weight, bias, D):
 
 
 def _matrix(M: int, N: int, dtype, like: torch.Tensor) -> torch.Tensor:
-    return torch.empty((M, N), dtype=dtype, device=like.device)
+    return like.new_empty((M, N), dtype=dtype)
 
 
 def _int8_rows(M: int, K: int, like: torch.Tensor):
@@ -479,7 +483,7 @@ def layer_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias
         with _there(stream, x):
             return layer_norm_int8(x, weight, bias, eps)
     q, ldq = _int8_rows(M, D, x)
-    scale = torch.empty(M, dtype=torch.float32, device=x.device)
+    scale = x.new_empty(M, dtype=torch.float32)
     _check(lib().twell_layer_norm_int8(x.data_ptr(), _DTYPES[x.dtype], ldx, w, b, wt, M, D, eps, q.data_ptr(), ldq,
                                        scale.data_ptr(), None, None, _here(x)), "twell_layer_norm_int8")
     return q, scale
@@ -511,7 +515,7 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: 
         pw, pb = dw.data_ptr(), db.data_ptr()
         if scratch is None:
             size = L.twell_layer_norm_bwd_scratch_bytes(M, D)
-            scratch = torch.empty(size, dtype=torch.uint8, device=x.device)
+            scratch = x.new_empty(size, dtype=torch.uint8)
         else:
             size = scratch.numel() * scratch.element_size()
         ps = scratch.data_ptr()
@@ -530,7 +534,7 @@ def quantize_rows(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Ten
         with _there(stream, x):
             return quantize_rows(x)
     q, ldq = _int8_rows(M, K, x)
-    scale = torch.empty(M, dtype=torch.float32, device=x.device)
+    scale = x.new_empty(M, dtype=torch.float32)
     _check(lib().twell_quantize_rows(x.data_ptr(), _DTYPES[x.dtype], ldx, M, K, q.data_ptr(), ldq, scale.data_ptr(),
                                      _here(x)), "twell_quantize_rows")
     return q, scale
