@@ -20,7 +20,7 @@ cudaError_t norm(const LayerNormParams& p, bool aligned, int sms, cudaStream_t s
   const int vectors = 2 * 4 * 8 * r.chunks * 32 * r.warps;
   int per_sm = norm_blocks(r.chunks);
   while (per_sm > 1 && per_sm * (kRowThreads / r.threads()) * (vectors + 2048) > 220 * 1024) --per_sm;
-  if (vectors > 48 * 1024) {  // else no attribute is needed
+  if (vectors > 40 * 1024) {  // up to 48 KB with the static part, no attribute is needed
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, vectors);
     if (e != cudaSuccess) return e;
   }
