@@ -64,9 +64,10 @@ struct LayerNormBwdParams {
   float inv_d;         // 1 / D
   int dy_type, x_type, w_type;
 };
-// Partial rows of the parameter gradients that a call writes.
-int layer_norm_bwd_parts(int M, int D, int sms);
-cudaError_t launch_layer_norm_bwd(const LayerNormBwdParams& p, int sms, cudaStream_t s);
+// Most partial rows of the parameter gradients that a call writes, for any alignment.
+int layer_norm_bwd_max_parts(int M, int D, int sms);
+// `parts`: the partial rows it writes.
+cudaError_t launch_layer_norm_bwd(const LayerNormBwdParams& p, int sms, int& parts, cudaStream_t s);
 cudaError_t launch_layer_norm_bwd_reduce(const LayerNormBwdParams& p, int parts, cudaStream_t s);
 
 struct QuantizeParams {

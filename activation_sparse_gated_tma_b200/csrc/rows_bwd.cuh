@@ -2,8 +2,8 @@
 //   dx = r (g - (sum g + xh sum g xh) / D),   dw = sum_rows dy xh,   db = sum_rows dy.
 // dw and db want a thread to keep its columns over many rows, so a row belongs
 // to a group of as many warps as it takes (a thread holds NC chunks of eight
-// columns), and what a row costs beyond its columns is shared by R rows at a
-// time: their 2 R sums go through one exchange and one barrier.  x and dy are
+// columns), and what a row costs beyond its columns is shared by R rows at a time
+// (two of aligned rows): their 2 R sums go through one exchange and one barrier.  x and dy are
 // read straight into registers, several rows' worth of bytes in flight per SM.
 // Bound by HBM for fp32 rows, by instruction issue for 16-bit ones.  Measured
 // before (fp32, 16384 x 2560): batches of rows through a shared-memory ring and
@@ -56,6 +56,38 @@ __device__ __forceinline__ void group_sums(const Group& g, int flip, BwdShared& 
   for (int k = 0; k < kValues; ++k) v[k] = __shfl_sync(0xffffffffu, s, k * kStep);
 }
 
+// Columns of a thread: eight neighbouring ones of aligned rows; of others every
+// T-th, read and written by elements, neighbouring lanes on neighbouring ones.
+template <bool ALIGNED>
+__device__ __forceinline__ int bwd_column(int t, int nt, int j, int i) {
+  return ALIGNED ? 8 * (t + j * nt) + i : (8 * j + i) * nt + t;
+}
+template <class T, bool ALIGNED>
+using BwdLayer = typename std::conditional<ALIGNED, Chunk<T>, Oct>::type;
+__device__ __forceinline__ Oct unpack8(const Oct& v) { return v; }
+template <class T, int NC, bool ALIGNED>
+__device__ __forceinline__ void load_bwd(const T* row, int D, int t, int nt, BwdLayer<T, ALIGNED> (&v)[NC]) {
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    if constexpr (ALIGNED) {
+      v[j] = load_chunk<T, true, false>(row, 0, 8 * (t + j * nt), D);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j].e[i] = bwd_column<false>(t, nt, j, i) < D ? to_f32(row[bwd_column<false>(t, nt, j, i)]) : 0.f;
+    }
+  }
+}
+template <class T, bool ALIGNED>
+__device__ __forceinline__ void store_bwd(T* row, int D, int t, int nt, int j, const Oct& o) {
+  if constexpr (ALIGNED) {
+    store_chunk<T, true, false>(row, 0, 8 * (t + j * nt), D, pack8<T>(o));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (bwd_column<false>(t, nt, j, i) < D) row[bwd_column<false>(t, nt, j, i)] = from_f32<T>(o.e[i]);
+  }
+}
+
 template <class TX, class TDY, int NC, int R, bool ALIGNED>
 __global__ void __maxnreg__(bwd_registers(NC))
     layer_norm_bwd_kernel(const LayerNormBwdParams p, const BwdPlan plan) {
@@ -76,7 +108,7 @@ __global__ void __maxnreg__(bwd_registers(NC))
   for (int j = 0; j < NC; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = 8 * (g.t + j * g.nt) + i;
+      const int c = bwd_column<ALIGNED>(g.t, g.nt, j, i);
       float e = 0.f;
       if (c < p.D)
         e = !p.weight                ? 1.f
@@ -88,20 +120,23 @@ __global__ void __maxnreg__(bwd_registers(NC))
     }
   const uint32_t step = gridDim.x * groups * R;
   for (uint32_t row0 = (blockIdx.x * groups + g.id) * R; row0 < p.M; row0 += step) {
-    RowPart<TX, NC> x[R];
-    RowPart<TDY, NC> dy[R];
+    BwdLayer<TX, ALIGNED> x[R][NC];
+    BwdLayer<TDY, ALIGNED> dy[R][NC];
     float mean[R], rstd[R], s[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (row0 + r < p.M) {
         const uint32_t row = row0 + r;
-        load_row<TX, NC, ALIGNED>(static_cast<const TX*>(p.x) + row * p.ldx, plan.whole_pieces(row), p.D, g.t, g.nt, x[r]);
-        load_row<TDY, NC, ALIGNED>(static_cast<const TDY*>(p.dy) + row * p.lddy, plan.whole_pieces(row), p.D, g.t, g.nt, dy[r]);
+        load_bwd<TX, NC, ALIGNED>(static_cast<const TX*>(p.x) + row * p.ldx, p.D, g.t, g.nt, x[r]);
+        load_bwd<TDY, NC, ALIGNED>(static_cast<const TDY*>(p.dy) + row * p.lddy, p.D, g.t, g.nt, dy[r]);
         mean[r] = p.mean[row];
         rstd[r] = p.rstd[row];
       } else {
-        x[r] = {};
-        dy[r] = {};
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          x[r][j] = {};
+          dy[r][j] = {};
+        }
         mean[r] = rstd[r] = 0.f;
       }
     }
@@ -120,7 +155,7 @@ __global__ void __maxnreg__(bwd_registers(NC))
       float a[2] = {0.f, 0.f}, b[2] = {0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
-        const Oct xv = unpack8(x[r].c[j]), dv = unpack8(dy[r].c[j]);
+        const Oct xv = unpack8(x[r][j]), dv = unpack8(dy[r][j]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float xh = (xv.e[i] - mean[r]) * rstd[r], gr = dv.e[i] * w[j].e[i];
@@ -141,15 +176,14 @@ __global__ void __maxnreg__(bwd_registers(NC))
       // dx = r g - r sum g / D - xh r sum g xh / D
       const float c1 = -rstd[r] * (s[2 * r] * p.inv_d), c2 = -rstd[r] * (s[2 * r + 1] * p.inv_d);
       TX* dx = static_cast<TX*>(p.dx) + static_cast<int64_t>(row0 + r) * p.lddx;
-      const uint32_t past = bytes_past(dx);
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
-        const Oct xv = unpack8(x[r].c[j]), dv = unpack8(dy[r].c[j]);
+        const Oct xv = unpack8(x[r][j]), dv = unpack8(dy[r][j]);
         Oct o;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           o.e[i] = fmaf((xv.e[i] - mean[r]) * rstd[r], c2, fmaf(dv.e[i] * w[j].e[i], rstd[r], c1));
-        store_layer<TX, NC, ALIGNED>(dx, past, p.D, g.t, g.nt, j, pack8<TX>(o));
+        store_bwd<TX, ALIGNED>(dx, p.D, g.t, g.nt, j, o);
       }
     }
   }
@@ -160,7 +194,7 @@ __global__ void __maxnreg__(bwd_registers(NC))
   for (int j = 0; j < NC; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = 8 * (g.t + j * g.nt) + i;
+      const int c = bwd_column<ALIGNED>(g.t, g.nt, j, i);
       if (c < p.D) {
         to[c] = dw[j].e[i];
         to[p.D + c] = db[j].e[i];

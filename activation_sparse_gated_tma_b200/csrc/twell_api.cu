@@ -1135,7 +1135,7 @@ twell_status twell_layer_norm_int8(const void* x, twell_dtype x_type, int64_t ld
 size_t twell_layer_norm_bwd_scratch_bytes(int M, int D) {
   DeviceInfo dev;
   if (M < 1 || D < 1 || D > kLayerNormMaxD || device_info(dev) != TWELL_OK) return 0;
-  return static_cast<size_t>(layer_norm_bwd_parts(M, D, dev.sms)) * 2 * D * sizeof(float);
+  return static_cast<size_t>(layer_norm_bwd_max_parts(M, D, dev.sms)) * 2 * D * sizeof(float);
 }
 
 twell_status twell_layer_norm_bwd(const void* dy, twell_dtype dy_type, int64_t lddy, const void* x, twell_dtype x_type,
@@ -1166,8 +1166,7 @@ twell_status twell_layer_norm_bwd(const void* dy, twell_dtype dy_type, int64_t l
   if (sums && !aligned16(scratch)) return fail(TWELL_ERR_INVALID, "scratch must be non-NULL and 16-byte aligned");
   DeviceInfo dev;
   if ((st = device_info(dev)) != TWELL_OK) return st;
-  const int parts = layer_norm_bwd_parts(M, D, dev.sms);
-  const size_t need = static_cast<size_t>(parts) * 2 * D * sizeof(float);
+  const size_t need = static_cast<size_t>(layer_norm_bwd_max_parts(M, D, dev.sms)) * 2 * D * sizeof(float);
   if (sums && scratch_bytes < need)
     return fail(TWELL_ERR_INVALID, "scratch too small: %zu < %zu bytes", scratch_bytes, need);
   LayerNormBwdParams p = {};
@@ -1176,8 +1175,9 @@ twell_status twell_layer_norm_bwd(const void* dy, twell_dtype dy_type, int64_t l
   p.dweight = dweight; p.dbias = dbias;
   p.lddy = lddy; p.ldx = ldx; p.lddx = lddx; p.M = M; p.D = D; p.inv_d = 1.f / D;
   p.dy_type = dy_type; p.x_type = x_type; p.w_type = w_type;
+  int parts = 0;
   TW_CUDA(trace_begin(stream));
-  TW_CUDA(launch_layer_norm_bwd(p, dev.sms, stream));
+  TW_CUDA(launch_layer_norm_bwd(p, dev.sms, parts, stream));
   TW_CUDA(trace_end(stream, "layer_norm_bwd"));
   if (sums) {
     TW_CUDA(trace_begin(stream));
