@@ -9,6 +9,7 @@ namespace twell {
 
 constexpr int kI8BK = 128;            // int8 elements per 128-byte swizzle row
 constexpr int kI8MaxK = 131071;       // 128 * 128 * K stays within a 32-bit sum
+constexpr int kI8MaxRows = 0x7fffffff - 1024;  // M and N: tile counts and padded rows stay within 32 bits
 constexpr int kI8ChannelTile = 128;   // rows of a weight box
 
 // y[m][n] = f(x_scale[m] w_scale[n] sum_k x[m][k] w[n][k]); plain: + bias[n];

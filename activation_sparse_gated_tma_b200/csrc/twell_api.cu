@@ -117,24 +117,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // Row-major [outer][inner] matrix of `type` elements of `bytes` bytes, rows
-// ld_bytes apart; box [box_outer][128 bytes], 128-byte swizzle, zero fill out
-// of bounds.  Cached by (device, pointer, shape, stride, type, box).
-twell_status tmap_rows(const void* ptr, CUtensorMapDataType type, uint64_t bytes, uint64_t inner, uint64_t outer,
-                       uint64_t ld_bytes, uint32_t box_outer, CUtensorMap& out) {
-  using Key = std::tuple<int, uintptr_t, uint64_t, uint64_t, uint64_t, int, uint32_t>;
-  static std::mutex mu;
-  static std::map<Key, CUtensorMap> cache;
-  int dev = 0;
-  TW_CUDA(cudaGetDevice(&dev));
-  const Key key{dev, reinterpret_cast<uintptr_t>(ptr), inner, outer, ld_bytes, static_cast<int>(type), box_outer};
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    auto it = cache.find(key);
-    if (it != cache.end()) {
-      out = it->second;
-      return TWELL_OK;
-    }
-  }
+// ld_bytes apart; box [box_outer][128 bytes], 128-byte swizzle, zero fill out of bounds.
+twell_status encode_rows(const void* ptr, CUtensorMapDataType type, uint64_t bytes, uint64_t inner, uint64_t outer,
+                         uint64_t ld_bytes, uint32_t box_outer, CUtensorMap& out) {
   auto enc = encode_fn();
   if (!enc) return fail(TWELL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   cuuint64_t dims[2] = {inner, outer};
@@ -144,14 +129,31 @@ twell_status tmap_rows(const void* ptr, CUtensorMapDataType type, uint64_t bytes
   CUresult r = enc(&out, type, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(TWELL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return TWELL_OK;
+}
+
+// bf16 row-major [outer][inner] matrix.  Cached by (device, pointer, shape, box).
+twell_status tmap_bf16(const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_outer, CUtensorMap& out) {
+  using Key = std::tuple<int, uintptr_t, uint64_t, uint64_t, uint32_t>;
+  static std::mutex mu;
+  static std::map<Key, CUtensorMap> cache;
+  int dev = 0;
+  TW_CUDA(cudaGetDevice(&dev));
+  const Key key{dev, reinterpret_cast<uintptr_t>(ptr), inner, outer, box_outer};
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    auto it = cache.find(key);
+    if (it != cache.end()) {
+      out = it->second;
+      return TWELL_OK;
+    }
+  }
+  const twell_status st = encode_rows(ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, outer, inner * 2, box_outer, out);
+  if (st != TWELL_OK) return st;
   std::lock_guard<std::mutex> lock(mu);
   if (cache.size() > 4096) cache.clear();
   cache.emplace(key, out);
   return TWELL_OK;
-}
-
-twell_status tmap_bf16(const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_outer, CUtensorMap& out) {
-  return tmap_rows(ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, outer, inner * 2, box_outer, out);
 }
 
 // ---------------------------------------------------------------- buffer layout
@@ -584,6 +586,16 @@ twell_status dense_ffn_impl(const uint16_t* x, const uint16_t* wg_t, const uint1
   return TWELL_OK;
 }
 
+// A C entry lets no exception out (the caches' maps allocate).
+template <class F>
+twell_status no_throw(F call) {
+  try {
+    return call();
+  } catch (...) {
+    return fail(TWELL_ERR_CUDA, "out of host memory");
+  }
+}
+
 // ---------------------------------------------------------------- rows of activations
 int type_bytes(int type) { return type == TWELL_F32 ? 4 : type == TWELL_I8 ? 1 : 2; }
 bool floating(int type) { return type == TWELL_F32 || type == TWELL_BF16 || type == TWELL_F16; }
@@ -647,8 +659,9 @@ twell_status int8_product(const int8_t* x, int64_t ldx, const float* x_scale, co
                           const float* bias, bool gated, int M, int N, int K, void* y, int y_type, int64_t ldy,
                           cudaStream_t stream) {
   g_launches = 0;
-  if (M < 0 || N < 1 || K < 1 || K > kI8MaxK)
-    return fail(TWELL_ERR_INVALID, "invalid sizes M=%d N=%d K=%d (need M >= 0, N >= 1, 1 <= K <= %d)", M, N, K, kI8MaxK);
+  if (M < 0 || M > kI8MaxRows || N < 1 || N > kI8MaxRows || K < 1 || K > kI8MaxK)
+    return fail(TWELL_ERR_INVALID, "invalid sizes M=%d N=%d K=%d (need 0 <= M <= %d, 1 <= N <= %d, 1 <= K <= %d)", M, N,
+                K, kI8MaxRows, kI8MaxRows, kI8MaxK);
   if (!floating(y_type)) return fail(TWELL_ERR_INVALID, "unsupported output type %d", y_type);
   if (M == 0) return TWELL_OK;
   twell_status st;
@@ -664,11 +677,14 @@ twell_status int8_product(const int8_t* x, int64_t ldx, const float* x_scale, co
   const bool aligned_rows = aligned16(y) && (ldy * type_bytes(y_type)) % 16 == 0;
   const Int8Plan plan = int8_plan(M, N, K, gated, aligned_rows, dev.sms);
   CUtensorMap tm_x, tm_w, tm_w2;
-  if ((st = tmap_rows(x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, M, ldx, int8_token_box(plan), tm_x)) != TWELL_OK) return st;
-  if ((st = tmap_rows(w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, ldw, kI8ChannelBox, tm_w)) != TWELL_OK) return st;
+  // (Encoded for every call, a fraction of a microsecond: activations move.)
+  auto encode = [](const int8_t* q, int64_t ld, int rows, int cols, int box, CUtensorMap& out) {
+    return encode_rows(q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, cols, rows, ld, box, out);
+  };
+  if ((st = encode(x, ldx, M, K, int8_token_box(plan), tm_x)) != TWELL_OK) return st;
+  if ((st = encode(w, ldw, N, K, kI8ChannelBox, tm_w)) != TWELL_OK) return st;
   tm_w2 = tm_w;
-  if (gated && (st = tmap_rows(w2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, K, N, ldw2, kI8ChannelBox, tm_w2)) != TWELL_OK)
-    return st;
+  if (gated && (st = encode(w2, ldw2, N, K, kI8ChannelBox, tm_w2)) != TWELL_OK) return st;
   Int8GemmParams p = {};
   p.x_scale = x_scale; p.w_scale = w_scale; p.w2_scale = w2_scale; p.bias = bias;
   p.y = y; p.ldy = ldy; p.M = M; p.N = N; p.K = K; p.y_type = y_type;
@@ -1123,18 +1139,22 @@ twell_status twell_layer_norm_fwd(const void* x, twell_dtype x_type, int64_t ldx
                                   twell_dtype w_type, int M, int D, float eps, void* y, twell_dtype y_type, int64_t ldy,
                                   float* mean, float* rstd, cudaStream_t stream) {
   if (!floating(y_type)) return g_launches = 0, fail(TWELL_ERR_INVALID, "unsupported output type %d", y_type);
-  return layer_norm_impl(x, x_type, ldx, weight, bias, w_type, M, D, eps, y, y_type, ldy, nullptr, mean, rstd, stream);
+  return no_throw([&] {
+    return layer_norm_impl(x, x_type, ldx, weight, bias, w_type, M, D, eps, y, y_type, ldy, nullptr, mean, rstd, stream);
+  });
 }
 
 twell_status twell_layer_norm_int8(const void* x, twell_dtype x_type, int64_t ldx, const void* weight, const void* bias,
                                    twell_dtype w_type, int M, int D, float eps, int8_t* q, int64_t ldq, float* scale,
                                    float* mean, float* rstd, cudaStream_t stream) {
-  return layer_norm_impl(x, x_type, ldx, weight, bias, w_type, M, D, eps, q, TWELL_I8, ldq, scale, mean, rstd, stream);
+  return no_throw([&] {
+    return layer_norm_impl(x, x_type, ldx, weight, bias, w_type, M, D, eps, q, TWELL_I8, ldq, scale, mean, rstd, stream);
+  });
 }
 
 size_t twell_layer_norm_bwd_scratch_bytes(int M, int D) {
   DeviceInfo dev;
-  if (M < 1 || D < 1 || D > kLayerNormMaxD || device_info(dev) != TWELL_OK) return 0;
+  if (M < 1 || D < 1 || D > kLayerNormMaxD || no_throw([&] { return device_info(dev); }) != TWELL_OK) return 0;
   return static_cast<size_t>(layer_norm_bwd_max_parts(M, D, dev.sms)) * 2 * D * sizeof(float);
 }
 
@@ -1142,102 +1162,113 @@ twell_status twell_layer_norm_bwd(const void* dy, twell_dtype dy_type, int64_t l
                                   int64_t ldx, const float* mean, const float* rstd, const void* weight,
                                   twell_dtype w_type, int M, int D, void* dx, int64_t lddx, float* dweight, float* dbias,
                                   void* scratch, size_t scratch_bytes, cudaStream_t stream) {
-  g_launches = 0;
-  if (M < 0 || D < 1 || D > kLayerNormMaxD)
-    return fail(TWELL_ERR_INVALID, "invalid sizes M=%d D=%d (need M >= 0, 1 <= D <= %d)", M, D, kLayerNormMaxD);
-  if (!floating(x_type) || !pairs_with(x_type, dy_type))
-    return fail(TWELL_ERR_INVALID, "unsupported types: x %d, dy %d", x_type, dy_type);
-  if (weight && !floating(w_type)) return fail(TWELL_ERR_INVALID, "unsupported weight type %d", w_type);
-  if ((dweight && !element_aligned(dweight, TWELL_F32)) || (dbias && !element_aligned(dbias, TWELL_F32)))
-    return fail(TWELL_ERR_INVALID, "dweight and dbias must be 4-byte aligned");
-  if (M == 0) {
-    if (dweight) TW_CUDA(cudaMemsetAsync(dweight, 0, static_cast<size_t>(D) * sizeof(float), stream));
-    if (dbias) TW_CUDA(cudaMemsetAsync(dbias, 0, static_cast<size_t>(D) * sizeof(float), stream));
-    return TWELL_OK;
-  }
-  twell_status st;
-  if ((st = check_rows("dy", dy, dy_type, lddy, D)) != TWELL_OK) return st;
-  if ((st = check_rows("x", x, x_type, ldx, D)) != TWELL_OK) return st;
-  if ((st = check_rows("dx", dx, x_type, lddx, D)) != TWELL_OK) return st;
-  if (!element_aligned(mean, TWELL_F32) || !element_aligned(rstd, TWELL_F32))
-    return fail(TWELL_ERR_INVALID, "mean and rstd must be non-NULL and 4-byte aligned");
-  if (weight && !element_aligned(weight, w_type)) return fail(TWELL_ERR_INVALID, "weight must be aligned to its elements");
-  const bool sums = dweight || dbias;
-  if (sums && !aligned16(scratch)) return fail(TWELL_ERR_INVALID, "scratch must be non-NULL and 16-byte aligned");
-  DeviceInfo dev;
-  if ((st = device_info(dev)) != TWELL_OK) return st;
-  const size_t need = static_cast<size_t>(layer_norm_bwd_max_parts(M, D, dev.sms)) * 2 * D * sizeof(float);
-  if (sums && scratch_bytes < need)
-    return fail(TWELL_ERR_INVALID, "scratch too small: %zu < %zu bytes", scratch_bytes, need);
-  LayerNormBwdParams p = {};
-  p.dy = dy; p.x = x; p.weight = weight; p.mean = mean; p.rstd = rstd; p.dx = dx;
-  p.partial = sums ? static_cast<float*>(scratch) : nullptr;
-  p.dweight = dweight; p.dbias = dbias;
-  p.lddy = lddy; p.ldx = ldx; p.lddx = lddx; p.M = M; p.D = D; p.inv_d = 1.f / D;
-  p.dy_type = dy_type; p.x_type = x_type; p.w_type = w_type;
-  int parts = 0;
-  TW_CUDA(trace_begin(stream));
-  TW_CUDA(launch_layer_norm_bwd(p, dev.sms, parts, stream));
-  TW_CUDA(trace_end(stream, "layer_norm_bwd"));
-  if (sums) {
+  return no_throw([&]() -> twell_status {
+    g_launches = 0;
+    if (M < 0 || D < 1 || D > kLayerNormMaxD)
+      return fail(TWELL_ERR_INVALID, "invalid sizes M=%d D=%d (need M >= 0, 1 <= D <= %d)", M, D, kLayerNormMaxD);
+    if (!floating(x_type) || !pairs_with(x_type, dy_type))
+      return fail(TWELL_ERR_INVALID, "unsupported types: x %d, dy %d", x_type, dy_type);
+    if (weight && !floating(w_type)) return fail(TWELL_ERR_INVALID, "unsupported weight type %d", w_type);
+    if ((dweight && !element_aligned(dweight, TWELL_F32)) || (dbias && !element_aligned(dbias, TWELL_F32)))
+      return fail(TWELL_ERR_INVALID, "dweight and dbias must be 4-byte aligned");
+    if (M == 0) {
+      if (dweight) TW_CUDA(cudaMemsetAsync(dweight, 0, static_cast<size_t>(D) * sizeof(float), stream));
+      if (dbias) TW_CUDA(cudaMemsetAsync(dbias, 0, static_cast<size_t>(D) * sizeof(float), stream));
+      return TWELL_OK;
+    }
+    twell_status st;
+    if ((st = check_rows("dy", dy, dy_type, lddy, D)) != TWELL_OK) return st;
+    if ((st = check_rows("x", x, x_type, ldx, D)) != TWELL_OK) return st;
+    if ((st = check_rows("dx", dx, x_type, lddx, D)) != TWELL_OK) return st;
+    if (!element_aligned(mean, TWELL_F32) || !element_aligned(rstd, TWELL_F32))
+      return fail(TWELL_ERR_INVALID, "mean and rstd must be non-NULL and 4-byte aligned");
+    if (weight && !element_aligned(weight, w_type)) return fail(TWELL_ERR_INVALID, "weight must be aligned to its elements");
+    const bool sums = dweight || dbias;
+    if (sums && !aligned16(scratch)) return fail(TWELL_ERR_INVALID, "scratch must be non-NULL and 16-byte aligned");
+    DeviceInfo dev;
+    if ((st = device_info(dev)) != TWELL_OK) return st;
+    const size_t need = static_cast<size_t>(layer_norm_bwd_max_parts(M, D, dev.sms)) * 2 * D * sizeof(float);
+    if (sums && scratch_bytes < need)
+      return fail(TWELL_ERR_INVALID, "scratch too small: %zu < %zu bytes", scratch_bytes, need);
+    LayerNormBwdParams p = {};
+    p.dy = dy; p.x = x; p.weight = weight; p.mean = mean; p.rstd = rstd; p.dx = dx;
+    p.partial = sums ? static_cast<float*>(scratch) : nullptr;
+    p.dweight = dweight; p.dbias = dbias;
+    p.lddy = lddy; p.ldx = ldx; p.lddx = lddx; p.M = M; p.D = D; p.inv_d = 1.f / D;
+    p.dy_type = dy_type; p.x_type = x_type; p.w_type = w_type;
+    int parts = 0;
     TW_CUDA(trace_begin(stream));
-    TW_CUDA(launch_layer_norm_bwd_reduce(p, parts, stream));
-    TW_CUDA(trace_end(stream, "layer_norm_bwd_reduce"));
-  }
-  return TWELL_OK;
+    TW_CUDA(launch_layer_norm_bwd(p, dev.sms, parts, stream));
+    TW_CUDA(trace_end(stream, "layer_norm_bwd"));
+    if (sums) {
+      TW_CUDA(trace_begin(stream));
+      TW_CUDA(launch_layer_norm_bwd_reduce(p, parts, stream));
+      TW_CUDA(trace_end(stream, "layer_norm_bwd_reduce"));
+    }
+    return TWELL_OK;
+  });
 }
 
 twell_status twell_quantize_rows(const void* x, twell_dtype x_type, int64_t ldx, int M, int K, int8_t* q, int64_t ldq,
                                  float* scale, cudaStream_t stream) {
-  g_launches = 0;
-  if (M < 0 || K < 1 || K > kI8MaxK)
-    return fail(TWELL_ERR_INVALID, "invalid sizes M=%d K=%d (need M >= 0, 1 <= K <= %d)", M, K, kI8MaxK);
-  if (!floating(x_type)) return fail(TWELL_ERR_INVALID, "unsupported type %d", x_type);
-  if (M == 0) return TWELL_OK;
-  twell_status st;
-  if ((st = check_rows("x", x, x_type, ldx, K)) != TWELL_OK) return st;
-  if ((st = check_rows("q", q, TWELL_I8, ldq, K)) != TWELL_OK) return st;
-  if (!element_aligned(scale, TWELL_F32)) return fail(TWELL_ERR_INVALID, "scale must be non-NULL and 4-byte aligned");
-  DeviceInfo dev;
-  if ((st = device_info(dev)) != TWELL_OK) return st;
-  const QuantizeParams p{x, q, scale, ldx, ldq, M, K, x_type};
-  TW_CUDA(trace_begin(stream));
-  TW_CUDA(launch_quantize_rows(p, dev.sms, stream));
-  TW_CUDA(trace_end(stream, "quantize_rows"));
-  return TWELL_OK;
+  return no_throw([&]() -> twell_status {
+    g_launches = 0;
+    if (M < 0 || K < 1 || K > kI8MaxK)
+      return fail(TWELL_ERR_INVALID, "invalid sizes M=%d K=%d (need M >= 0, 1 <= K <= %d)", M, K, kI8MaxK);
+    if (!floating(x_type)) return fail(TWELL_ERR_INVALID, "unsupported type %d", x_type);
+    if (M == 0) return TWELL_OK;
+    twell_status st;
+    if ((st = check_rows("x", x, x_type, ldx, K)) != TWELL_OK) return st;
+    if ((st = check_rows("q", q, TWELL_I8, ldq, K)) != TWELL_OK) return st;
+    if (!element_aligned(scale, TWELL_F32)) return fail(TWELL_ERR_INVALID, "scale must be non-NULL and 4-byte aligned");
+    DeviceInfo dev;
+    if ((st = device_info(dev)) != TWELL_OK) return st;
+    const QuantizeParams p{x, q, scale, ldx, ldq, M, K, x_type};
+    TW_CUDA(trace_begin(stream));
+    TW_CUDA(launch_quantize_rows(p, dev.sms, stream));
+    TW_CUDA(trace_end(stream, "quantize_rows"));
+    return TWELL_OK;
+  });
 }
 
 twell_status twell_dequantize_rows(const int8_t* q, int64_t ldq, const float* scale, int M, int K, void* y,
                                    twell_dtype y_type, int64_t ldy, cudaStream_t stream) {
-  g_launches = 0;
-  if (M < 0 || K < 1 || K > kI8MaxK)
-    return fail(TWELL_ERR_INVALID, "invalid sizes M=%d K=%d (need M >= 0, 1 <= K <= %d)", M, K, kI8MaxK);
-  if (!floating(y_type)) return fail(TWELL_ERR_INVALID, "unsupported type %d", y_type);
-  if (M == 0) return TWELL_OK;
-  twell_status st;
-  if ((st = check_rows("q", q, TWELL_I8, ldq, K)) != TWELL_OK) return st;
-  if ((st = check_rows("y", y, y_type, ldy, K)) != TWELL_OK) return st;
-  if (!element_aligned(scale, TWELL_F32)) return fail(TWELL_ERR_INVALID, "scale must be non-NULL and 4-byte aligned");
-  DeviceInfo dev;
-  if ((st = device_info(dev)) != TWELL_OK) return st;
-  const QuantizeParams p{q, y, const_cast<float*>(scale), ldq, ldy, M, K, y_type};
-  TW_CUDA(trace_begin(stream));
-  TW_CUDA(launch_dequantize_rows(p, dev.sms, stream));
-  TW_CUDA(trace_end(stream, "dequantize_rows"));
-  return TWELL_OK;
+  return no_throw([&]() -> twell_status {
+    g_launches = 0;
+    if (M < 0 || K < 1 || K > kI8MaxK)
+      return fail(TWELL_ERR_INVALID, "invalid sizes M=%d K=%d (need M >= 0, 1 <= K <= %d)", M, K, kI8MaxK);
+    if (!floating(y_type)) return fail(TWELL_ERR_INVALID, "unsupported type %d", y_type);
+    if (M == 0) return TWELL_OK;
+    twell_status st;
+    if ((st = check_rows("q", q, TWELL_I8, ldq, K)) != TWELL_OK) return st;
+    if ((st = check_rows("y", y, y_type, ldy, K)) != TWELL_OK) return st;
+    if (!element_aligned(scale, TWELL_F32)) return fail(TWELL_ERR_INVALID, "scale must be non-NULL and 4-byte aligned");
+    DeviceInfo dev;
+    if ((st = device_info(dev)) != TWELL_OK) return st;
+    const QuantizeParams p{q, y, const_cast<float*>(scale), ldq, ldy, M, K, y_type};
+    TW_CUDA(trace_begin(stream));
+    TW_CUDA(launch_dequantize_rows(p, dev.sms, stream));
+    TW_CUDA(trace_end(stream, "dequantize_rows"));
+    return TWELL_OK;
+  });
 }
 
 twell_status twell_int8_linear(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w, int64_t ldw,
                                const float* w_scale, const float* bias, int M, int N, int K, void* y,
                                twell_dtype y_type, int64_t ldy, cudaStream_t stream) {
-  return int8_product(x, ldx, x_scale, w, ldw, w_scale, nullptr, 0, nullptr, bias, false, M, N, K, y, y_type, ldy, stream);
+  return no_throw([&] {
+    return int8_product(x, ldx, x_scale, w, ldw, w_scale, nullptr, 0, nullptr, bias, false, M, N, K, y, y_type, ldy,
+                        stream);
+  });
 }
 
 twell_status twell_int8_gated(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* wg, int64_t ldwg,
                               const float* wg_scale, const int8_t* wu, int64_t ldwu, const float* wu_scale, int M, int N,
                               int K, void* h, twell_dtype h_type, int64_t ldh, cudaStream_t stream) {
-  return int8_product(x, ldx, x_scale, wg, ldwg, wg_scale, wu, ldwu, wu_scale, nullptr, true, M, N, K, h, h_type, ldh,
-                      stream);
+  return no_throw([&] {
+    return int8_product(x, ldx, x_scale, wg, ldwg, wg_scale, wu, ldwu, wu_scale, nullptr, true, M, N, K, h, h_type, ldh,
+                        stream);
+  });
 }
 
 twell_status dense_ffn_fwd(const uint16_t* x, const uint16_t* wg_t, const uint16_t* wu_t, const uint16_t* wd, int M,

@@ -281,10 +281,11 @@ twell_status dense_ffn_fwd_noalloc(const uint16_t* x, const uint16_t* wg_t, cons
  * Conventions of the calls from here to twell_int8_gated, beyond those above:
  *   - a matrix argument is a pointer, and a row stride `ld*` in elements (at
  *     least the row length); a row's elements are contiguous.  Pointers need
- *     only their element's alignment unless a call says more; rows whose base
- *     and stride are multiples of 16 bytes take 16-byte accesses.
- *   - outputs are overwritten and must not overlap inputs; bytes between rows
- *     are neither read nor written.
+ *     only their element's alignment unless a call says more; matrices whose
+ *     rows all start on 16 bytes (8 of int8) and have a multiple of eight
+ *     elements are the fast ones.
+ *   - outputs are overwritten and must not overlap inputs; bytes between the
+ *     rows of an output are not written, those of an input not used.
  *   - M = 0 is valid and launches nothing.
  *   - repeated calls on one device give the same bits.
  */
@@ -350,9 +351,9 @@ twell_status twell_dequantize_rows(const int8_t* q, int64_t ldq, const float* sc
  * The sum is exact (32-bit integers, K <= 131071); scaling is fp32 in the order
  * written and y is rounded once to y_type (F32, BF16, F16).  x [M][K], w [N][K]
  * int8 (all values -128..127): 16-byte aligned, row strides multiples of 16; K
- * itself and N may be any number >= 1 (what lies between a row's end and the
- * next row is not read as data).  bias [N] fp32 or NULL.  No workspace.  Every
- * wait inside is bounded; a tile whose wait gave up is written as NaN.
+ * itself, M and N (up to 2^31 - 1025) may be any number.  bias [N] fp32 or
+ * NULL.  No workspace.  Every wait inside is bounded; a tile whose wait gave up
+ * is written as NaN.
  */
 twell_status twell_int8_linear(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w, int64_t ldw,
                                const float* w_scale, const float* bias, int M, int N, int K, void* y,

@@ -145,6 +145,22 @@ def test_int8_products_on_another_stream_and_in_graphs():
         assert all(torch.equal(a, c) for a, c in zip(ref, outs[k]))
 
 
+def test_offsets_past_32_bits():
+    # Rows 2 GiB apart: the third one's offset passes 2^32 bytes, the output's 2^32 elements' bytes too.
+    far = (1 << 31) + 32
+    xb = torch.zeros(2 * far + 96, dtype=torch.int8, device="cuda")
+    x = torch.as_strided(xb, (3, 96), (far, 1))
+    q, xs = _operand(3, 96, 1)
+    x.copy_(q)
+    w, ws = _operand(40, 96, 2)
+    yb = torch.zeros(2 * far + 40, dtype=BF16, device="cuda")
+    y = torch.as_strided(yb, (3, 40), (far, 1))
+    tw.int8_linear(x, xs, w, ws, out=y)
+    assert torch.equal(y, tw.int8_linear(q, xs, w, ws))
+    wide = torch.as_strided(xb, (3, 96), (far, 1))
+    assert torch.equal(tw.int8_linear(q, xs, wide, xs), tw.int8_linear(q, xs, q, xs))
+
+
 # ---------------------------------------------------------------- as used together
 def _ffn_inputs(M, K, N, seed):
     w = wl.Workload(f"int8_{M}_{K}_{N}", M, K, N, 128, 16, seed, p_mean=0.05)

@@ -303,6 +303,25 @@ def test_layer_norm_int8(M, D, dtype, gap):
     assert int(q.abs().max()) == 127 or not bool(amax.any())
 
 
+def test_offsets_past_32_bits():
+    # Rows 2^31 elements apart: the third one's offset passes 2^32 bytes and elements.
+    far = (1 << 31) + 16
+    buf = torch.zeros(2 * far + 520, dtype=BF16, device="cuda")
+    x = torch.as_strided(buf, (3, 520), (far, 1))
+    near = _rows(3, 520, BF16)
+    x.copy_(near)
+    w, b = _affine(520, F32)
+    y, mean, rstd = tw.layer_norm(near, w, b, stats=True)
+    assert torch.equal(tw.layer_norm(x, w, b), y)
+    assert all(torch.equal(p, q) for p, q in zip(tw.layer_norm_int8(x, w, b), tw.layer_norm_int8(near, w, b)))
+    assert all(torch.equal(p, q) for p, q in zip(tw.quantize_rows(x), tw.quantize_rows(near)))
+    dy = _rows(3, 520, F32, seed=5)
+    assert all(torch.equal(p, q) for p, q in zip(tw.layer_norm_bwd(dy, x, mean, rstd, w),
+                                                 tw.layer_norm_bwd(dy, near, mean, rstd, w)))
+    tw.layer_norm(near, w, b, out=x)
+    assert torch.equal(x, y)
+
+
 # ---------------------------------------------------------------- streams, graphs
 def test_rows_on_another_stream_and_in_graphs():
     x = _rows(64, 1000, F32)

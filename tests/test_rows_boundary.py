@@ -74,7 +74,7 @@ def test_quantize_and_dequantize_refuse():
 
 
 @pytest.mark.parametrize("bad", [
-    dict(M=-1), dict(N=0), dict(K=0), dict(K=131072), dict(x=None), dict(w=None), dict(xs=None), dict(ws=None),
+    dict(M=-1), dict(N=0), dict(K=0), dict(K=131072), dict(M=(1 << 31) - 1), dict(N=(1 << 31) - 1), dict(x=None), dict(w=None), dict(xs=None), dict(ws=None),
     dict(y=None), dict(x=P + 8), dict(w=P + 8), dict(ldx=72), dict(ldw=72), dict(ldx=48), dict(ldw=48), dict(xs=P + 2),
     dict(ws=P + 2), dict(bias=P + 2), dict(yt=I8), dict(yt=-1), dict(y=P + 1), dict(ldy=31)])
 def test_int8_products_refuse(bad):
