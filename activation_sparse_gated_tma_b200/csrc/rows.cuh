@@ -133,9 +133,36 @@ __device__ __forceinline__ uint32_t bytes_past(const T* row) {
   return static_cast<uint32_t>(reinterpret_cast<uint64_t>(row)) & (sizeof(typename Chunk<T>::Piece) - 1);
 }
 
+// A whole chunk in one access: 16 bytes of 16-bit elements, 32 of fp32 (as two
+// of 16 every sector went to L2 twice: backward fp32 16384 x 2560 moved 1.4 GB
+// there instead of 0.5).
+__device__ __forceinline__ Chunk<float> load_whole(const float* p) {
+  Chunk<float> v;
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v.p[0].x), "=r"(v.p[0].y), "=r"(v.p[0].z), "=r"(v.p[0].w), "=r"(v.p[1].x), "=r"(v.p[1].y),
+                 "=r"(v.p[1].z), "=r"(v.p[1].w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void store_whole(float* p, const Chunk<float>& v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v.p[0].x), "r"(v.p[0].y),
+               "r"(v.p[0].z), "r"(v.p[0].w), "r"(v.p[1].x), "r"(v.p[1].y), "r"(v.p[1].z), "r"(v.p[1].w)
+               : "memory");
+}
+template <class T>
+__device__ __forceinline__ Chunk<T> load_whole(const T* p) {
+  Chunk<T> v;
+  v.p[0] = *reinterpret_cast<const typename Chunk<T>::Piece*>(p);
+  return v;
+}
+template <class T>
+__device__ __forceinline__ void store_whole(T* p, const Chunk<T>& v) {
+  *reinterpret_cast<typename Chunk<T>::Piece*>(p) = v.p[0];
+}
+
 // This lane's chunk, at column c, of a row of D elements in global memory;
 // columns from D on are 0.  FULL: no lane of the warp reaches D.  ALIGNED rows
-// start on pieces and have whole chunks.  Else the row starts `past` bytes
+// start on whole chunks' sizes and have whole chunks.  Else the row starts `past` bytes
 // behind a piece, and pieces that hold bytes of the row are read whole (rows
 // for which one would reach outside the matrix are not read this way).
 template <class T, bool ALIGNED, bool FULL>
@@ -144,10 +171,7 @@ __device__ __forceinline__ Chunk<T> load_chunk(const T* row, uint32_t past, int 
   using Piece = typename C::Piece;
   C v = {};
   if (ALIGNED) {
-    if (FULL || c < D) {
-#pragma unroll
-      for (int i = 0; i < C::kPieces; ++i) v.p[i] = reinterpret_cast<const Piece*>(row + c)[i];
-    }
+    if (FULL || c < D) v = load_whole(row + c);
     return v;
   }
   const int lane = threadIdx.x & 31;
@@ -194,10 +218,7 @@ __device__ __forceinline__ void store_chunk(T* row, uint32_t past, int c, int D,
   using C = Chunk<T>;
   using Piece = typename C::Piece;
   if (ALIGNED) {
-    if (FULL || c < D) {
-#pragma unroll
-      for (int i = 0; i < C::kPieces; ++i) reinterpret_cast<Piece*>(row + c)[i] = v.p[i];
-    }
+    if (FULL || c < D) store_whole(row + c, v);
     return;
   }
   const int lane = threadIdx.x & 31;
@@ -224,14 +245,6 @@ __device__ __forceinline__ void store_chunk(T* row, uint32_t past, int c, int D,
       if ((e < head || e >= tail) && e < n) row[c + i] = chunk_element(v, i);
     }
   }
-}
-
-// Keeps the compiler from carrying a chunk's unpacked elements from one pass
-// over a row to the next: unpacking again costs an instruction per element,
-// holding both forms costs the registers of a third or fourth block per SM.
-template <class T>
-__device__ __forceinline__ void forget_unpacked(Chunk<T>& c) {
-  if constexpr (sizeof(T) == 2) asm volatile("" : "+r"(c.p[0].x), "+r"(c.p[0].y), "+r"(c.p[0].z), "+r"(c.p[0].w));
 }
 
 // ---------------------------------------------------------------- a thread's part of a row
@@ -408,6 +421,31 @@ __device__ __forceinline__ float max_abs(float m, const Oct& v) {
   for (int i = 0; i < 8; ++i) m = max_abs(m, v.e[i]);
   return m;
 }
+// Over the chunks of a row; 16-bit elements two at a time as they are packed.
+template <class T, int NC>
+__device__ __forceinline__ float max_abs(RowPart<T, NC>& r) {
+  if constexpr (sizeof(T) == 4) {
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) m = max_abs(m, unpack8(r.c[j]));
+    return m;
+  } else {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    union { uint32_t u; T2 v; } m, e;
+    m.u = 0;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const uint32_t w[4] = {r.c[j].p[0].x, r.c[j].p[0].y, r.c[j].p[0].z, r.c[j].p[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        e.u = w[i] & 0x7fff7fffu;
+        m.v = __hmax2_nan(m.v, e.v);
+      }
+    }
+    const float2 f = unpack2(m.u, T());
+    return max_abs(f.x, f.y);
+  }
+}
 // This thread's elements of a row, layer j's given by get(j), to int8 and into the row.
 template <int NC, bool ALIGNED, class Get>
 __device__ __forceinline__ void store_row_i8(int8_t* row, int D, int t, int nt, const RowScale& r, Get get) {
@@ -529,12 +567,7 @@ __global__ void __launch_bounds__(kRowThreads, quantize_blocks(NC, sizeof(TI)))
     load_row<TI, NC, ALIGNED>(static_cast<const TI*>(p.x) + row * p.ldx, plan.whole_pieces(row), p.K, g.t, g.nt, v);
     if ((!ALIGNED || NC <= 2) && g.t == 0 && plan.whole_pieces(row + step))
       prefetch_row(static_cast<const TI*>(p.x) + (row + step) * p.ldx, p.K);
-    float m = 0.f;
-#pragma unroll
-    for (int j = 0; j < NC; ++j) m = max_abs(m, unpack8(v.c[j]));
-    const RowScale r = row_scale(group_max(g, m));
-#pragma unroll
-    for (int j = 0; j < NC; ++j) forget_unpacked(v.c[j]);
+    const RowScale r = row_scale(group_max(g, max_abs(v)));
     store_row_i8<NC, ALIGNED>(static_cast<int8_t*>(p.y) + row * p.ldy, p.K, g.t, g.nt, r,
                               [&](int j) { return unpack8(v.c[j]); });
     if (g.t == 0) p.scale[row] = r.scale;
@@ -570,9 +603,12 @@ __global__ void __launch_bounds__(kRowThreads) quantize_long_rows_kernel(const Q
   }
 }
 
-// x = q s.  Blocks of `across` threads along a row, eight columns each at a
-// time, by 256 / across rows.  A byte becomes fp32 without a conversion: with
-// its sign bit flipped it is the last byte of 2^23 + q + 128.
+// x = q s.  A block takes a segment of `across` chunks of 4 * 256 / across rows,
+// a thread the same chunk of four of them, so that its loads are in flight
+// together whatever the row's length (with neighbouring chunks of one row
+// instead, rows of 256 took 19 us for 65536 and rows of 2560 30 us for 16384).
+// A byte becomes fp32 without a conversion: with its sign bit flipped it is
+// the last byte of 2^23 + q + 128.
 __device__ __forceinline__ Oct dequantize8(uint2 word, float s) {
   const uint32_t u[2] = {word.x ^ 0x80808080u, word.y ^ 0x80808080u};
   Oct v;
@@ -586,28 +622,33 @@ template <class TO, bool Q_ALIGNED, bool ALIGNED>
 __global__ void __launch_bounds__(256) dequantize_rows_kernel(const QuantizeParams p, int across) {
   griddep_launch_dependents();
   griddep_wait();
+  constexpr int kRows = 4;
   const int tx = static_cast<int>(threadIdx.x) % across, ty = static_cast<int>(threadIdx.x) / across;
   const int high = 256 / across;
-  constexpr int kAhead = 3;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * high + ty; row < p.M; row += static_cast<int64_t>(gridDim.x) * high) {
-    const int8_t* q = static_cast<const int8_t*>(p.x) + row * p.ldx;
-    TO* y = static_cast<TO*>(p.y) + row * p.ldy;
-    const uint32_t past = bytes_past(y);
-    const float s = p.scale[row];
-    // Whole warps take part in every step, up to the row's last column.
-    for (int c0 = 0; c0 < p.K; c0 += across * 8 * kAhead) {
-      Chunk<int8_t> in[kAhead];
+  const int segments = (p.K + 8 * across - 1) / (8 * across);
+  const int64_t blocks = (static_cast<int64_t>(p.M) + kRows * high - 1) / (kRows * high) * segments;
+  for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
+    const int64_t row0 = block / segments * (kRows * high) + ty;  // then every high-th
+    const int c = (static_cast<int>(block % segments) * across + tx) * 8;
+    Chunk<int8_t> in[kRows];
+    float s[kRows];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int c = c0 + 8 * (tx + k * across);
-        if (Q_ALIGNED && c + 8 <= p.K)
-          in[k].p[0] = *reinterpret_cast<const uint2*>(q + c);
-        else
-          in[k] = load_elements(q, c, p.K);
-      }
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t row = row0 + r * high;
+      if (row >= p.M) break;
+      const int8_t* q = static_cast<const int8_t*>(p.x) + row * p.ldx;
+      s[r] = p.scale[row];
+      if (Q_ALIGNED && c + 8 <= p.K)
+        in[r].p[0] = *reinterpret_cast<const uint2*>(q + c);
+      else
+        in[r] = load_elements(q, c, p.K);
+    }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        store_chunk<TO, ALIGNED, false>(y, past, c0 + 8 * (tx + k * across), p.K, pack8<TO>(dequantize8(in[k].p[0], s)));
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t row = row0 + r * high;
+      if (row >= p.M) break;
+      TO* y = static_cast<TO*>(p.y) + row * p.ldy;
+      store_chunk<TO, ALIGNED, false>(y, bytes_past(y), c, p.K, pack8<TO>(dequantize8(in[r].p[0], s[r])));
     }
   }
 }

@@ -78,9 +78,8 @@ int layer_norm_bwd_max_parts(int M, int D, int sms) {
 }
 
 cudaError_t launch_layer_norm_bwd(const LayerNormBwdParams& p, int sms, int& parts, cudaStream_t s) {
-  const bool vec = p.D % 8 == 0 && aligned_rows(p.x, p.ldx * type_size(p.x_type), 16) &&
-                   aligned_rows(p.dx, p.lddx * type_size(p.x_type), 16) &&
-                   aligned_rows(p.dy, p.lddy * type_size(p.dy_type), 16);
+  const bool vec = p.D % 8 == 0 && chunk_rows(p.x, p.ldx, p.x_type) && chunk_rows(p.dx, p.lddx, p.x_type) &&
+                   chunk_rows(p.dy, p.lddy, p.dy_type);
   if (p.x_type == TWELL_F32) {
     if (p.dy_type == TWELL_F32) return norm_bwd<float, float>(p, vec, sms, parts, s);
     if (p.dy_type == TWELL_BF16) return norm_bwd<float, bf16>(p, vec, sms, parts, s);

@@ -24,7 +24,7 @@ cudaError_t quantize(const QuantizeParams& p, bool aligned, int sms, cudaStream_
 }  // namespace
 
 cudaError_t launch_quantize_rows(const QuantizeParams& p, int sms, cudaStream_t s) {
-  const bool vec = p.K % 8 == 0 && aligned_rows(p.x, p.ldx * type_size(p.type), 16) && aligned_rows(p.y, p.ldy, 8);
+  const bool vec = p.K % 8 == 0 && chunk_rows(p.x, p.ldx, p.type) && chunk_rows(p.y, p.ldy, TWELL_I8);
   if (p.type == TWELL_F32) return quantize<float>(p, vec, sms, s);
   if (p.type == TWELL_BF16) return quantize<bf16>(p, vec, sms, s);
   return quantize<__half>(p, vec, sms, s);
@@ -32,12 +32,15 @@ cudaError_t launch_quantize_rows(const QuantizeParams& p, int sms, cudaStream_t 
 
 template <class TO>
 static cudaError_t dequantize(const QuantizeParams& p, int sms, cudaStream_t s) {
-  const bool q_aligned = aligned_rows(p.x, p.ldx, 8);
-  const bool vec = p.K % 8 == 0 && aligned_rows(p.y, p.ldy * type_size(p.type), 16);
-  const int across = p.K > 4096 ? 256 : p.K > 2048 ? 128 : p.K > 1024 ? 64 : 32;  // two to four chunks a thread
-  const int high = 256 / across;
-  const int64_t need = (static_cast<int64_t>(p.M) + high - 1) / high;
-  const int grid = static_cast<int>(need < 64 * sms ? need : 64 * sms);
+  const bool q_aligned = chunk_rows(p.x, p.ldx, TWELL_I8);
+  const bool vec = p.K % 8 == 0 && chunk_rows(p.y, p.ldy, p.type);
+  // Threads along a row: the number that leaves the fewest of them idle in the last segment.
+  const int chunks = (p.K + 7) / 8;
+  int across = 256;
+  for (int a = 128; a >= 32; a /= 2)
+    if ((chunks + a - 1) / a * a < (chunks + across - 1) / across * across) across = a;
+  const int64_t blocks = (static_cast<int64_t>(p.M) + 4 * (256 / across) - 1) / (4 * (256 / across)) * ((chunks + across - 1) / across);
+  const int grid = static_cast<int>(blocks < 16 * sms ? blocks : 16 * sms);
   auto kern = q_aligned ? (vec ? dequantize_rows_kernel<TO, true, true> : dequantize_rows_kernel<TO, true, false>)
                         : (vec ? dequantize_rows_kernel<TO, false, true> : dequantize_rows_kernel<TO, false, false>);
   return launch_pdl(kern, grid, 256, 0, s, p, across);

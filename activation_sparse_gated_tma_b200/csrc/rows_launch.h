@@ -12,6 +12,9 @@ inline bool aligned_rows(const void* p, int64_t ld_bytes, int to) {
   return (reinterpret_cast<uintptr_t>(p) % to) == 0 && ld_bytes % to == 0;
 }
 inline int type_size(int type) { return type == TWELL_F32 ? 4 : type == TWELL_I8 ? 1 : 2; }
+// Whether a matrix's rows all start on the size of eight elements (32 bytes of fp32, 16, 8 of int8).
+inline bool chunk_rows(const void* p, int64_t ld, int type) { return aligned_rows(p, ld * type_size(type), 8 * type_size(type)); }
+
 // The rows of a matrix whose whole 16-byte pieces lie between its first and
 // its last element: all but a few at either end, narrowed into [begin, end).
 inline void rows_inside(const void* p, int64_t ld, int M, int D, int type, uint32_t& begin, uint32_t& end) {

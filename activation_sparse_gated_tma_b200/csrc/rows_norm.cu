@@ -30,8 +30,7 @@ cudaError_t norm(const LayerNormParams& p, bool aligned, int sms, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_layer_norm(const LayerNormParams& p, int sms, cudaStream_t s) {
-  const bool vec = p.D % 8 == 0 && aligned_rows(p.x, p.ldx * type_size(p.x_type), 16) &&
-                   aligned_rows(p.y, p.ldy * type_size(p.y_type), p.y_type == TWELL_I8 ? 8 : 16);
+  const bool vec = p.D % 8 == 0 && chunk_rows(p.x, p.ldx, p.x_type) && chunk_rows(p.y, p.ldy, p.y_type);
   if (p.y_type == TWELL_I8) {
     if (p.x_type == TWELL_F32) return norm<float, int8_t>(p, vec, sms, s);
     if (p.x_type == TWELL_BF16) return norm<bf16, int8_t>(p, vec, sms, s);

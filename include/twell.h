@@ -282,8 +282,8 @@ twell_status dense_ffn_fwd_noalloc(const uint16_t* x, const uint16_t* wg_t, cons
  *   - a matrix argument is a pointer, and a row stride `ld*` in elements (at
  *     least the row length); a row's elements are contiguous.  Pointers need
  *     only their element's alignment unless a call says more; matrices whose
- *     rows all start on 16 bytes (8 of int8) and have a multiple of eight
- *     elements are the fast ones.
+ *     rows have a multiple of eight elements and all start on the size of eight
+ *     (32 bytes of fp32, 16 of 16-bit types, 8 of int8) are the fast ones.
  *   - outputs are overwritten and must not overlap inputs; bytes between the
  *     rows of an output are not written, those of an input not used.
  *   - M = 0 is valid and launches nothing.
