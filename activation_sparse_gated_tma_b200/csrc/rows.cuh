@@ -287,18 +287,38 @@ __device__ __forceinline__ void prefetch_row(const T* row, int D) {
 }
 
 // A parameter vector of D elements into `padded` floats of shared memory, by
-// the whole block; `fill` where p is NULL, 0 from D on.  place(c): where column c goes.
-template <class Place>
-__device__ __forceinline__ void stage_vector(const void* p, int type, float fill, int D, int padded, float* to, Place place) {
-  for (int c = threadIdx.x; c < padded; c += blockDim.x) {
-    float e = 0.f;
-    if (c < D)
-      e = !p                   ? fill
-          : type == TWELL_F32  ? static_cast<const float*>(p)[c]
-          : type == TWELL_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(p)[c])
-                               : to_f32(static_cast<const __half*>(p)[c]);
-    to[place(c)] = e;
+// the whole block, several loads in flight; `fill` where p is NULL, 0 from D
+// on.  nt > 0: each layer of 8 nt columns with the first halves of its chunks
+// before the second ones.  (Not inlined: the kernels have no registers to spare.)
+template <class T>
+__device__ __forceinline__ void stage_typed(const T* p, float fill, int D, int padded, float* to, int nt) {
+  constexpr int kAhead = 8;
+  for (int c0 = threadIdx.x; c0 < padded; c0 += kAhead * blockDim.x) {
+    float e[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int c = c0 + k * blockDim.x;
+      e[k] = c >= D ? 0.f : p ? to_f32(p[c]) : fill;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      int c = c0 + k * blockDim.x;
+      if (c >= padded) break;
+      if (nt > 0) {
+        const int layer = c / (8 * nt), in = c - layer * 8 * nt;
+        c = layer * 8 * nt + ((in >> 2) & 1) * 4 * nt + (in >> 3) * 4 + (in & 3);
+      }
+      to[c] = e[k];
+    }
   }
+}
+static __device__ __noinline__ void stage_vector(const void* p, int type, float fill, int D, int padded, float* to, int nt) {
+  if (type == TWELL_F32)
+    stage_typed(static_cast<const float*>(p), fill, D, padded, to, nt);
+  else if (type == TWELL_BF16)
+    stage_typed(static_cast<const __nv_bfloat16*>(p), fill, D, padded, to, nt);
+  else
+    stage_typed(static_cast<const __half*>(p), fill, D, padded, to, nt);
 }
 
 // ---------------------------------------------------------------- groups
@@ -479,15 +499,11 @@ __global__ void __launch_bounds__(kRowThreads, norm_blocks(NC))
   const int padded = 8 * NC * g.nt;  // whole layers, read without a check
   griddep_launch_dependents();
   griddep_wait();
-  {
-    const int span = 8 * g.nt;
-    auto place = [&](int c) {
-      const int layer = c / span, in = c - layer * span;
-      return layer * span + ((in >> 2) & 1) * 4 * g.nt + (in >> 3) * 4 + (in & 3);
-    };
-    stage_vector(p.weight, p.w_type, 1.f, p.D, padded, vectors, place);
-    stage_vector(p.bias, p.w_type, 0.f, p.D, padded, vectors + padded, place);
-  }
+  // The first row on its way while the vectors are staged.
+  if (g.t == 0 && plan.whole_pieces(blockIdx.x * groups + g.id))
+    prefetch_row(static_cast<const TI*>(p.x) + (blockIdx.x * groups + g.id) * p.ldx, p.D);
+  stage_vector(p.weight, p.w_type, 1.f, p.D, padded, vectors, g.nt);
+  stage_vector(p.bias, p.w_type, 0.f, p.D, padded, vectors + padded, g.nt);
   __syncthreads();
   for (uint32_t row = blockIdx.x * groups + g.id; row < p.M; row += step) {
     Oct v[NC];
