@@ -13,6 +13,8 @@ constexpr int kMaxGroupWarps = 8;    // of a row
 constexpr int kNormChunks = 10;      // of eight elements that a thread holds at most
 constexpr int kNormChunksUnaligned = 6;  // joining pieces wants more warps (bf16, 8191 x 4095: 80 us with 10, 62 with 6)
 constexpr int kQuantizeChunks = 6;   // as long as kMaxGroupWarps warps hold the row so
+constexpr int kNormFewWarps = 8;     // per SM, up to which a row is spread over more warps than hold it
+constexpr int kQuantizeFewWarps = 32;
 constexpr int kBwdThreads = 512;     // of a block at most, backward
 constexpr int kLayerNormMaxD = 16384;
 constexpr int kQuantizeMaxRow = 8 * kNormChunks * kRowThreads;  // longer rows are read twice

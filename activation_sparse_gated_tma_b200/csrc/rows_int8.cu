@@ -8,7 +8,7 @@ template <class TI>
 cudaError_t quantize(const QuantizeParams& p, bool aligned, int sms, cudaStream_t s) {
   if (p.K > kQuantizeMaxRow)
     return launch_pdl(quantize_long_rows_kernel<TI>, p.M < 4 * sms ? p.M : 4 * sms, kRowThreads, 0, s, p);
-  const RowShape r = row_shape(p.M, p.K, kQuantizeChunks, sms);
+  const RowShape r = row_shape(p.M, p.K, kQuantizeChunks, kQuantizeFewWarps, sms);
   RowPlan plan{r.warps, 0, static_cast<uint32_t>(p.M)};
   rows_inside(p.x, p.ldx, p.M, p.K, p.type, plan.begin, plan.end);
   void (*kern)(const QuantizeParams, const RowPlan) = nullptr;
