@@ -374,17 +374,26 @@ __device__ __forceinline__ float group_max(Group& g, float magnitude) {
 
 // ---------------------------------------------------------------- quantisation
 // One row's scale.  q is the integer nearest to 127 x / amax, ties to even,
-// exactly.  inv = 127 / amax in fp32 is within 2^-24 of the quotient's factor,
-// so the true quotient lies between x low and x high, low and high 2^-22 below
-// and above inv.  Adding 1.5 * 2^23 rounds both to integers (held in the sum's
-// low byte); where they agree that is the answer, else the sign of
-// 254 x - (2 q + 1) amax decides between q and q + 1.  Rows near either end of
-// the exponents' range are scaled by 2^100 or 2^-100 first.  A row with a NaN or
-// an infinity gets scale NaN and q = 0, one of zeros scale 0.
+// exactly, found by adding 1.5 * 2^23, which rounds to an integer held in the
+// sum's low byte.
+// fp32 values: 127 / amax in fp32 is within 2^-24 of the quotient's factor, so
+// the true quotient lies between x low and x high, low and high 2^-22 below and
+// above it.  Where both round to the same integer that is the answer, else the
+// sign of 254 x - (2 q + 1) amax decides between q and q + 1.
+// 16-bit values (NARROW): ties are frequent (x = amax / 2 is one), but what is
+// none is far from one.  254 x - (2 q + 1) amax is a multiple of x's last bit and
+// x has 11 bits at most, so a quotient next to a tie is off by at least
+// 1 / (254 * 2047) of it: 16 units of its last fp32 place.  The factor
+// (127 + 2^-15) / amax puts x's product (2.016 -+ 0.5) m -+ 0.5 units, 1 <= m < 2,
+// above the true quotient (0.5 m the factor's rounding, 0.5 the product's), and
+// clearing the last three bits takes a tie back to itself and all others to their side of it.
+// Rows near either end of the exponents' range are scaled by 2^100 or 2^-100
+// first.  A row with a NaN or an infinity gets scale NaN and q = 0, one of zeros scale 0.
 struct RowScale {
   float amax, low, high, scale, up;
   bool none;
 };
+template <bool NARROW>
 __device__ __forceinline__ RowScale row_scale(float amax) {
   RowScale r;
   const bool finite = amax <= 3.402823466e38f;  // a NaN is not
@@ -392,9 +401,13 @@ __device__ __forceinline__ RowScale row_scale(float amax) {
   r.none = !finite || amax == 0.f;
   r.up = amax < 0x1p-100f ? 0x1p100f : amax > 0x1p100f ? 0x1p-100f : 1.f;
   r.amax = amax * r.up;
-  const float inv = 127.f / r.amax;
-  r.low = inv * (1.f - 0x1p-22f);
-  r.high = inv * (1.f + 0x1p-22f);
+  if (NARROW) {
+    r.low = r.high = (127.f + 0x1p-15f) / r.amax;
+  } else {
+    const float inv = 127.f / r.amax;
+    r.low = inv * (1.f - 0x1p-22f);
+    r.high = inv * (1.f + 0x1p-22f);
+  }
   return r;
 }
 __device__ __forceinline__ uint32_t pack_low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -411,22 +424,30 @@ __device__ __forceinline__ uint32_t nearest(float x, uint32_t a, uint32_t b, flo
   return static_cast<uint32_t>(q + (a != b && (t > 0.f || (t == 0.f && (q & 1))) ? 1 : 0));
 }
 // Eight values to eight bytes.
+template <bool NARROW>
 __device__ __forceinline__ uint2 quantize8(Oct v, const RowScale& r) {
   if (r.none) return make_uint2(0, 0);
   if (r.up != 1.f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v.e[i] *= r.up;
   }
-  uint32_t q[8], h[8], differ = 0;
+  uint32_t q[8];
+  if constexpr (NARROW) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    q[i] = __float_as_uint(fmaf(v.e[i], r.low, 12582912.f));
-    h[i] = __float_as_uint(fmaf(v.e[i], r.high, 12582912.f));
-    differ |= q[i] ^ h[i];
-  }
-  if (differ) {
+    for (int i = 0; i < 8; ++i)
+      q[i] = __float_as_uint(__uint_as_float(__float_as_uint(v.e[i] * r.low) & ~7u) + 12582912.f);
+  } else {
+    uint32_t h[8], differ = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = nearest(v.e[i], q[i], h[i], r.amax);
+    for (int i = 0; i < 8; ++i) {
+      q[i] = __float_as_uint(fmaf(v.e[i], r.low, 12582912.f));
+      h[i] = __float_as_uint(fmaf(v.e[i], r.high, 12582912.f));
+      differ |= q[i] ^ h[i];
+    }
+    if (differ) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = nearest(v.e[i], q[i], h[i], r.amax);
+    }
   }
   return make_uint2(pack_low_bytes(q[0], q[1], q[2], q[3]), pack_low_bytes(q[4], q[5], q[6], q[7]));
 }
@@ -467,13 +488,13 @@ __device__ __forceinline__ float max_abs(RowPart<T, NC>& r) {
   }
 }
 // This thread's elements of a row, layer j's given by get(j), to int8 and into the row.
-template <int NC, bool ALIGNED, class Get>
+template <int NC, bool ALIGNED, bool NARROW, class Get>
 __device__ __forceinline__ void store_row_i8(int8_t* row, int D, int t, int nt, const RowScale& r, Get get) {
   const uint32_t past = bytes_past(row);
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     Chunk<int8_t> q;
-    q.p[0] = quantize8(get(j), r);
+    q.p[0] = quantize8<NARROW>(get(j), r);
     store_layer<int8_t, NC, ALIGNED>(row, past, D, t, nt, j, q);
   }
 }
@@ -553,8 +574,8 @@ __global__ void __launch_bounds__(kRowThreads, norm_blocks(NC))
         // Behind the row the weight and the bias are 0, unless the row has no finite mean.
         m = max_abs(m, v[j]);
       }
-      const RowScale r = row_scale(group_max(g, m));
-      store_row_i8<NC, ALIGNED>(y, p.D, g.t, g.nt, r, [&](int j) { return v[j]; });
+      const RowScale r = row_scale<false>(group_max(g, m));
+      store_row_i8<NC, ALIGNED, false>(y, p.D, g.t, g.nt, r, [&](int j) { return v[j]; });
       if (g.t == 0) p.y_scale[row] = r.scale;
     } else {
       const uint32_t past = bytes_past(y);
@@ -583,8 +604,8 @@ __global__ void __launch_bounds__(kRowThreads, quantize_blocks(NC, sizeof(TI)))
     load_row<TI, NC, ALIGNED>(static_cast<const TI*>(p.x) + row * p.ldx, plan.whole_pieces(row), p.K, g.t, g.nt, v);
     if ((!ALIGNED || NC <= 2) && g.t == 0 && plan.whole_pieces(row + step))
       prefetch_row(static_cast<const TI*>(p.x) + (row + step) * p.ldx, p.K);
-    const RowScale r = row_scale(group_max(g, max_abs(v)));
-    store_row_i8<NC, ALIGNED>(static_cast<int8_t*>(p.y) + row * p.ldy, p.K, g.t, g.nt, r,
+    const RowScale r = row_scale<sizeof(TI) == 2>(group_max(g, max_abs(v)));
+    store_row_i8<NC, ALIGNED, sizeof(TI) == 2>(static_cast<int8_t*>(p.y) + row * p.ldy, p.K, g.t, g.nt, r,
                               [&](int j) { return unpack8(v.c[j]); });
     if (g.t == 0) p.scale[row] = r.scale;
   }
@@ -604,13 +625,13 @@ __global__ void __launch_bounds__(kRowThreads) quantize_long_rows_kernel(const Q
     float m = 0.f;
 #pragma unroll 16
     for (int c = g.t; c < p.K; c += kRowThreads) m = max_abs(m, to_f32(x[c]));
-    const RowScale r = row_scale(group_max(g, m));
+    const RowScale r = row_scale<sizeof(TI) == 2>(group_max(g, m));
     for (int c = g.t; c < p.K; c += 8 * kRowThreads) {
       Oct v;
 #pragma unroll
       for (int i = 0; i < 8; ++i) v.e[i] = c + i * kRowThreads < p.K ? to_f32(x[c + i * kRowThreads]) : 0.f;
       Chunk<int8_t> q;
-      q.p[0] = quantize8(v, r);
+      q.p[0] = quantize8<sizeof(TI) == 2>(v, r);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (c + i * kRowThreads < p.K) y[c + i * kRowThreads] = chunk_element(q, i);
@@ -641,30 +662,33 @@ __global__ void __launch_bounds__(256) dequantize_rows_kernel(const QuantizePara
   constexpr int kRows = 4;
   const int tx = static_cast<int>(threadIdx.x) % across, ty = static_cast<int>(threadIdx.x) / across;
   const int high = 256 / across;
+  const int64_t step_x = high * p.ldx, step_y = high * p.ldy;
   const int segments = (p.K + 8 * across - 1) / (8 * across);
-  const int64_t blocks = (static_cast<int64_t>(p.M) + kRows * high - 1) / (kRows * high) * segments;
-  for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
-    const int64_t row0 = block / segments * (kRows * high) + ty;  // then every high-th
-    const int c = (static_cast<int>(block % segments) * across + tx) * 8;
-    Chunk<int8_t> in[kRows];
-    float s[kRows];
+  for (int segment = blockIdx.x; segment < segments; segment += gridDim.x) {
+    const int c = (segment * across + tx) * 8;
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.y) * (kRows * high) + ty; row0 < p.M;
+         row0 += static_cast<int64_t>(gridDim.y) * (kRows * high)) {  // then every high-th
+      const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), (p.M - row0 + high - 1) / high));
+      const int8_t* q = static_cast<const int8_t*>(p.x) + row0 * p.ldx;
+      TO* y = static_cast<TO*>(p.y) + row0 * p.ldy;
+      Chunk<int8_t> in[kRows];
+      float s[kRows];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int64_t row = row0 + r * high;
-      if (row >= p.M) break;
-      const int8_t* q = static_cast<const int8_t*>(p.x) + row * p.ldx;
-      s[r] = p.scale[row];
-      if (Q_ALIGNED && c + 8 <= p.K)
-        in[r].p[0] = *reinterpret_cast<const uint2*>(q + c);
-      else
-        in[r] = load_elements(q, c, p.K);
-    }
+      for (int r = 0; r < kRows; ++r) {
+        if (r >= rows) break;
+        s[r] = p.scale[row0 + r * high];
+        if (Q_ALIGNED && c + 8 <= p.K)
+          in[r].p[0] = *reinterpret_cast<const uint2*>(q + c);
+        else
+          in[r] = load_elements(q, c, p.K);
+        q += step_x;
+      }
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int64_t row = row0 + r * high;
-      if (row >= p.M) break;
-      TO* y = static_cast<TO*>(p.y) + row * p.ldy;
-      store_chunk<TO, ALIGNED, false>(y, bytes_past(y), c, p.K, pack8<TO>(dequantize8(in[r].p[0], s[r])));
+      for (int r = 0; r < kRows; ++r) {
+        if (r >= rows) break;
+        store_chunk<TO, ALIGNED, false>(y, bytes_past(y), c, p.K, pack8<TO>(dequantize8(in[r].p[0], s[r])));
+        y += step_y;
+      }
     }
   }
 }

@@ -39,8 +39,10 @@ static cudaError_t dequantize(const QuantizeParams& p, int sms, cudaStream_t s) 
   int across = 256;
   for (int a = 128; a >= 32; a /= 2)
     if ((chunks + a - 1) / a * a < (chunks + across - 1) / across * across) across = a;
-  const int64_t blocks = (static_cast<int64_t>(p.M) + 4 * (256 / across) - 1) / (4 * (256 / across)) * ((chunks + across - 1) / across);
-  const int grid = static_cast<int>(blocks < 16 * sms ? blocks : 16 * sms);
+  const int segments = (chunks + across - 1) / across, rows = 4 * (256 / across);
+  const int gx = segments < 16 * sms ? segments : 16 * sms;
+  const int64_t need = (static_cast<int64_t>(p.M) + rows - 1) / rows, most = 16 * sms / gx;
+  const dim3 grid(gx, static_cast<unsigned>(need < most ? need : most));
   auto kern = q_aligned ? (vec ? dequantize_rows_kernel<TO, true, true> : dequantize_rows_kernel<TO, true, false>)
                         : (vec ? dequantize_rows_kernel<TO, false, true> : dequantize_rows_kernel<TO, false, false>);
   return launch_pdl(kern, grid, 256, 0, s, p, across);

@@ -274,6 +274,20 @@ def test_quantize_rows_ties_zeros_and_extremes():
     assert bool(scale[5:7].isnan().all()) and not q[5:7].any()
 
 
+@pytest.mark.parametrize("dtype,exponents", [(BF16, [0, 1, 3, 27, 28, 127, 227, 254]), (F16, [0, 1, 2, 15, 30])])
+def test_quantize_rows_every_16_bit_value(dtype, exponents):
+    """Rows of all values from amax down to below amax / 254, both signs, for
+    every mantissa of amax: with them every tie and every quotient next to one."""
+    ones = 128 if dtype == BF16 else 1024  # mantissas per exponent
+    for e in exponents:
+        top = (torch.arange(ones, device="cuda") + e * ones)[:, None]
+        bits = (top - torch.arange(9 * ones, device="cuda")[None]).clamp_min_(0).to(torch.int16)
+        x = torch.cat((bits, bits | -2 ** 15), 1).view(dtype)
+        q, scale = tw.quantize_rows(x)
+        ref, s = _quant64(x)
+        assert torch.equal(q.double(), ref) and torch.equal(scale, s), e
+
+
 def test_quantize_rows_leaves_the_padding_alone():
     L = tw.lib()
     x = _rows(5, 33, BF16)
