@@ -6,7 +6,7 @@ namespace {
 
 template <class TI, class TO>
 cudaError_t norm(const LayerNormParams& p, bool aligned, int sms, cudaStream_t s) {
-  const RowShape r = row_shape(p.M, p.D, aligned ? kNormChunks : kNormChunksUnaligned, kNormFewWarps, sms);
+  const RowShape r = row_shape(p.M, p.D, aligned ? kNormChunks : norm_chunks_unaligned(p.M, sms), kNormFewWarps, sms);
   RowPlan plan{r.warps, 0, static_cast<uint32_t>(p.M)};
   rows_inside(p.x, p.ldx, p.M, p.D, p.x_type, plan.begin, plan.end);
   void (*kern)(const LayerNormParams, const RowPlan) = nullptr;
