@@ -3,13 +3,14 @@
 //
 // All are bound by HBM: each row is read once, kept in registers and written
 // once.  What competes with the copies is instruction issue (at 6.5 TB/s an SM
-// has 290 cycles for a bf16 row of 2560), so the work per row that does not
+// has 450 cycles for a bf16 row of 2560), so the work per row that does not
 // depend on its length is kept small: a row belongs to as few warps as hold it
 // (one up to 2560 columns for the norm), more only while rows are too few for
-// the warps; 16-byte loads and stores, and eight to thirty-two warps per SM, are
-// all the memory parallelism it takes.  Measured before (bf16, 16384 x 2560,
-// norm): five warps per row 68 us, rows through a shared-memory ring of bulk
-// copies 36 us, this form 34 us; a copy of as many bytes takes 29 us.
+// the warps; 16-byte loads and stores, and 16 to 32 warps per SM, are all the
+// memory parallelism it takes.  Measured at 16384 x 2560: norm bf16 to bf16 33 us
+// (5.1 TB/s; five warps per row 68, rows through a shared-memory ring of bulk
+// copies 36), fp32 to bf16 45 us (5.7 TB/s), bf16 to int8 40 us; at 8192 x 5632,
+// bf16 to int8 rows 24 us (5.7 TB/s) and back 25.
 //
 // Columns of thread t in a group of T threads, layer j < NC, i < 8: 8 (t + j T) + i.
 // Rows that do not start on 16 bytes are read in aligned pieces, which
@@ -133,9 +134,8 @@ __device__ __forceinline__ uint32_t bytes_past(const T* row) {
   return static_cast<uint32_t>(reinterpret_cast<uint64_t>(row)) & (sizeof(typename Chunk<T>::Piece) - 1);
 }
 
-// A whole chunk in one access: 16 bytes of 16-bit elements, 32 of fp32 (as two
-// of 16 every sector went to L2 twice: backward fp32 16384 x 2560 moved 1.4 GB
-// there instead of 0.5).
+// A whole chunk in one access: 16 bytes of 16-bit elements, 32 of fp32 (backward
+// fp32 16384 x 2560: 84 us, as two of 16 88).
 __device__ __forceinline__ Chunk<float> load_whole(const float* p) {
   Chunk<float> v;
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -507,7 +507,7 @@ __device__ __forceinline__ void store_row_i8(int8_t* row, int D, int t, int nt, 
 // exact).  TO int8_t: y is quantised from its fp32 values, with one more
 // reduction for the row's largest magnitude.
 // The weight and the bias are staged in shared memory once per block (from
-// global memory every row's reads cost 4 us of the 34), each layer's first and
+// global memory every row's reads cost 4 us at bf16 16384 x 2560), each layer's first and
 // second halves of chunks apart, so that the lanes' 16-byte reads meet
 // different banks.
 template <class TI, class TO, int NC, bool ALIGNED>
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kRowThreads, norm_blocks(NC))
     {
       RowPart<TI, NC> raw;
       load_row<TI, NC, ALIGNED>(static_cast<const TI*>(p.x) + row * p.ldx, plan.whole_pieces(row), p.D, g.t, g.nt, raw);
-      // (Rows of many chunks keep enough loads in flight by themselves: 16384 x 2560 took 39 us with it, 36 without.)
+      // (Rows of many chunks keep enough loads in flight by themselves: bf16 16384 x 2560 took 3 us more with it.)
       if ((!ALIGNED || NC <= 2) && g.t == 0 && plan.whole_pieces(row + step))
         prefetch_row(static_cast<const TI*>(p.x) + (row + step) * p.ldx, p.D);
 #pragma unroll
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kRowThreads, norm_blocks(NC))
 }
 
 // ---------------------------------------------------------------- rows to int8 and back
-// The row stays packed in registers (few enough for 32 warps per SM) and is unpacked twice.
+// The row stays packed in registers (few enough for 32 warps per SM of 16-bit rows up to six chunks) and is unpacked twice.
 template <class TI, int NC, bool ALIGNED>
 __global__ void __launch_bounds__(kRowThreads, quantize_blocks(NC, sizeof(TI)))
     quantize_rows_kernel(const QuantizeParams p, const RowPlan plan) {
