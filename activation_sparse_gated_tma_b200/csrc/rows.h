@@ -25,7 +25,9 @@ constexpr int kQuantizeMaxRow = 8 * kNormChunks * kRowThreads;  // longer rows a
 constexpr int norm_blocks(int chunks) { return chunks <= 2 ? 4 : chunks <= 5 ? 3 : 2; }
 constexpr int quantize_blocks(int chunks, int element) { return chunks * element <= 12 ? 4 : chunks * element <= 20 ? 3 : 2; }
 
-constexpr int bwd_registers(int chunks) { return chunks == 1 ? 80 : 128; }
+// Registers of a thread, backward: chunks it holds of a row, rows at a time.  (Shifted rows take a warp more; with 72
+// registers three groups of nine fit an SM: fp16 16384 x 2047 70 us, with 80 83.)
+constexpr int bwd_registers(int chunks, int rows, bool shifted) { return chunks > 1 ? 128 : rows > 1 ? (shifted ? 72 : 80) : 64; }
 
 // How a launch lays out rows over blocks (see rows.cuh): warps per row; rows
 // [begin, end) are those whose aligned pieces lie inside the matrix.
@@ -34,7 +36,10 @@ struct RowPlan {
   uint32_t begin, end;
   __host__ __device__ bool whole_pieces(uint32_t row) const { return row >= begin && row < end; }
 };
-using BwdPlan = RowPlan;
+// Backward: shifted rows, `classes` of them by where a row starts (see rows_bwd.cuh).
+struct BwdPlan : RowPlan {
+  uint32_t classes;
+};
 
 // Rows are `ld` elements apart; a row's elements are contiguous.  Types are
 // twell_dtype values; out_type TWELL_I8 writes quantised rows and y_scale.

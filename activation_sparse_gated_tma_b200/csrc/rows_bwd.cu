@@ -17,7 +17,7 @@ __global__ void __launch_bounds__(32 * kReduceWarps)
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.f;
   if (c < 2 * static_cast<int64_t>(D))
-#pragma unroll 8
+#pragma unroll 16
     for (int r = warp; r < parts; r += kReduceWarps) s += partial[static_cast<int64_t>(r) * 2 * D + c];
   sums[warp][lane] = s;
   __syncthreads();
@@ -34,47 +34,84 @@ __global__ void __launch_bounds__(32 * kReduceWarps)
 }
 
 // Chunks a thread owns: the fewest of 1, 2, 4 with which kBwdThreads threads
-// own a row; two rows at a time where one chunk of aligned rows leaves the
-// registers for it (4099 x 2047, f16, unaligned: 39 us with two, 32 with one).
+// own a row; two rows at a time where one chunk (of rows not read by elements)
+// leaves the registers for it.
 struct BwdShape {
   int chunks, warps, groups, rows, grid;
 };
-BwdShape bwd_shape(int M, int D, bool aligned, int sms) {
+BwdShape bwd_shape(int M, int D, BwdRows kind, int classes, int sms) {
   BwdShape r;
-  r.chunks = D <= 8 * kBwdThreads ? 1 : D <= 16 * kBwdThreads ? 2 : 4;
-  r.rows = r.chunks == 1 && aligned ? 2 : 1;
-  r.warps = (D + 256 * r.chunks - 1) / (256 * r.chunks);
-  r.groups = r.warps < kMaxGroups ? kMaxGroups / r.warps : 1;
+  const int columns = kind == kShifted ? D + 7 : D;
+  r.chunks = columns <= 8 * kBwdThreads ? 1 : columns <= 16 * kBwdThreads ? 2 : 4;
+  r.warps = (columns + 256 * r.chunks - 1) / (256 * r.chunks);
+  r.rows = r.chunks == 1 && kind != kElements && 2 * 32 * r.warps * bwd_registers(1, 2, kind == kShifted) <= 65536 ? 2 : 1;
+  // As many groups as an SM's registers take, in as few blocks as hold them: each block leaves a partial row.
+  const int fit = 65536 / (32 * bwd_registers(r.chunks, r.rows, kind == kShifted)) / r.warps;
+  int per_sm = 1;
+  r.groups = 1;
+  for (int blocks = 1; blocks <= 4; ++blocks) {
+    const int groups = fit / blocks < kMaxGroups ? fit / blocks : kMaxGroups;
+    if (groups * blocks > r.groups * per_sm) {
+      r.groups = groups;
+      per_sm = blocks;
+    }
+  }
   const int64_t each = (static_cast<int64_t>(M) + static_cast<int64_t>(sms) * r.rows - 1) / (static_cast<int64_t>(sms) * r.rows);
   if (r.groups > each) r.groups = static_cast<int>(each);
-  const int threads = 32 * r.warps * r.groups;
-  const int resident = 65536 / bwd_registers(r.chunks);
-  const int per_sm = resident / threads > 1 ? resident / threads : 1;
-  const int64_t need = (static_cast<int64_t>(M) + r.groups * r.rows - 1) / (r.groups * r.rows);
-  const int64_t most = static_cast<int64_t>(sms) * per_sm;
-  r.grid = static_cast<int>(need < most ? need : most);
+  const int64_t of_class = (static_cast<int64_t>(M) + classes - 1) / classes;
+  const int64_t need = (of_class + r.groups * r.rows - 1) / (r.groups * r.rows);
+  const int64_t most = static_cast<int64_t>(sms) * per_sm / classes;
+  r.grid = static_cast<int>(need < most ? need : most) * classes;
   return r;
+}
+// Rows after which the place where a row starts within a chunk repeats.
+int shift_classes(int64_t ld) { return ld % 8 == 0 ? 1 : ld % 4 == 0 ? 2 : ld % 2 == 0 ? 4 : 8; }
+int shift_of(const void* p, int type) { return static_cast<int>(reinterpret_cast<uint64_t>(p) / type_size(type) % 8); }
+
+template <class TX, class TDY, BwdRows ROWS>
+void (*bwd_kernel(int chunks, int rows))(const LayerNormBwdParams, const BwdPlan) {
+  constexpr int kRows = ROWS == kElements ? 1 : 2;
+  return rows == 2     ? layer_norm_bwd_kernel<TX, TDY, 1, kRows, ROWS>
+         : chunks == 1 ? layer_norm_bwd_kernel<TX, TDY, 1, 1, ROWS>
+         : chunks == 2 ? layer_norm_bwd_kernel<TX, TDY, 2, 1, ROWS>
+                       : layer_norm_bwd_kernel<TX, TDY, 4, 1, ROWS>;
 }
 
 template <class TX, class TDY>
 cudaError_t norm_bwd(const LayerNormBwdParams& p, bool aligned, int sms, int& parts, cudaStream_t s) {
-  const BwdShape r = bwd_shape(p.M, p.D, aligned, sms);
+  const int x0 = shift_of(p.x, p.x_type);
+  const bool shifted = !aligned && shift_of(p.dx, p.x_type) == x0 && shift_of(p.dy, p.dy_type) == x0 &&
+                       p.lddx % 8 == p.ldx % 8 && p.lddy % 8 == p.ldx % 8 && p.D + 7 <= 32 * kBwdThreads;
+  const BwdRows kind = aligned ? kAligned : shifted ? kShifted : kElements;
+  const int classes = shifted ? shift_classes(p.ldx) : 1;
+  const BwdShape r = bwd_shape(p.M, p.D, kind, classes, sms);
   parts = r.grid;
-  BwdPlan plan{r.warps, 0, static_cast<uint32_t>(p.M)};
-  rows_inside(p.x, p.ldx, p.M, p.D, p.x_type, plan.begin, plan.end);
-  rows_inside(p.dy, p.lddy, p.M, p.D, p.dy_type, plan.begin, plan.end);
-  auto kern = r.chunks == 1   ? (aligned ? layer_norm_bwd_kernel<TX, TDY, 1, 2, true> : layer_norm_bwd_kernel<TX, TDY, 1, 1, false>)
-              : r.chunks == 2 ? (aligned ? layer_norm_bwd_kernel<TX, TDY, 2, 1, true> : layer_norm_bwd_kernel<TX, TDY, 2, 1, false>)
-                              : (aligned ? layer_norm_bwd_kernel<TX, TDY, 4, 1, true> : layer_norm_bwd_kernel<TX, TDY, 4, 1, false>);
-  const size_t smem = r.groups > 1 ? static_cast<size_t>(r.groups) * 2 * p.D * sizeof(float) : 0;  // 16 KB at most
+  BwdPlan plan{{r.warps, 0, static_cast<uint32_t>(p.M)}, static_cast<uint32_t>(classes)};
+  rows_inside(p.x, p.ldx, p.M, p.D, p.x_type, plan.begin, plan.end, shifted ? 8 * sizeof(TX) : 16);
+  rows_inside(p.dy, p.lddy, p.M, p.D, p.dy_type, plan.begin, plan.end, shifted ? 8 * sizeof(TDY) : 16);
+  const auto kern = kind == kAligned   ? bwd_kernel<TX, TDY, kAligned>(r.chunks, r.rows)
+                    : kind == kShifted ? bwd_kernel<TX, TDY, kShifted>(r.chunks, r.rows)
+                                       : bwd_kernel<TX, TDY, kElements>(r.chunks, r.rows);
+  const size_t smem = r.groups > 1 ? static_cast<size_t>(r.groups) * 2 * p.D * sizeof(float) : 0;
+  if (smem > 40 * 1024) {  // up to 48 KB with the static part, no attribute is needed
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
   return launch_pdl(kern, r.grid, 32 * r.warps * r.groups, smem, s, p, plan);
 }
 
 }  // namespace
 
 int layer_norm_bwd_max_parts(int M, int D, int sms) {
-  const int a = bwd_shape(M, D, true, sms).grid, b = bwd_shape(M, D, false, sms).grid;
-  return a > b ? a : b;
+  int most = bwd_shape(M, D, kAligned, 1, sms).grid;
+  const int elements = bwd_shape(M, D, kElements, 1, sms).grid;
+  if (elements > most) most = elements;
+  if (D + 7 <= 32 * kBwdThreads)
+    for (int classes = 1; classes <= 8; classes *= 2) {
+      const int shifted = bwd_shape(M, D, kShifted, classes, sms).grid;
+      if (shifted > most) most = shifted;
+    }
+  return most;
 }
 
 cudaError_t launch_layer_norm_bwd(const LayerNormBwdParams& p, int sms, int& parts, cudaStream_t s) {

@@ -15,13 +15,14 @@ inline int type_size(int type) { return type == TWELL_F32 ? 4 : type == TWELL_I8
 // Whether a matrix's rows all start on the size of eight elements (32 bytes of fp32, 16, 8 of int8).
 inline bool chunk_rows(const void* p, int64_t ld, int type) { return aligned_rows(p, ld * type_size(type), 8 * type_size(type)); }
 
-// The rows of a matrix whose whole 16-byte pieces lie between its first and
+// The rows of a matrix whose whole pieces (of `piece` bytes) lie between its first and
 // its last element: all but a few at either end, narrowed into [begin, end).
-inline void rows_inside(const void* p, int64_t ld, int M, int D, int type, uint32_t& begin, uint32_t& end) {
+inline void rows_inside(const void* p, int64_t ld, int M, int D, int type, uint32_t& begin, uint32_t& end,
+                        uint64_t piece = 16) {
   const uint64_t base = reinterpret_cast<uint64_t>(p), step = static_cast<uint64_t>(ld) * type_size(type);
   const uint64_t bytes = static_cast<uint64_t>(D) * type_size(type), last = base + (M - 1) * step + bytes;
-  while (begin < end && ((base + begin * step) & ~uint64_t(15)) < base) ++begin;
-  while (begin < end && ((base + (end - 1) * step + bytes + 15) & ~uint64_t(15)) > last) --end;
+  while (begin < end && ((base + begin * step) & ~(piece - 1)) < base) ++begin;
+  while (begin < end && ((base + (end - 1) * step + bytes + piece - 1) & ~(piece - 1)) > last) --end;
 }
 
 // Warps per row, chunks per thread, rows (groups) per block.

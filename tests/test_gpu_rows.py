@@ -144,6 +144,35 @@ def test_layer_norm_bwd(M, D, tx, td):
     _bwd(_rows(M, D, tx), _rows(M, D, td, seed=5), _affine(D, F32)[0])
 
 
+@pytest.mark.parametrize("M,D,tx,td", [(4099, 2047, F16, F16), (1030, 1535, BF16, F32), (1, 9, F32, F32), (7, 2049, F32, BF16),
+                                       (40, 4089, BF16, BF16), (40, 4090, F32, F32), (17, 8188, F16, F32), (6, 16377, F32, F32),
+                                       (300, 12, BF16, BF16), (2000, 514, F32, F32), (11, 16378, BF16, F32)])
+def test_layer_norm_bwd_rows_that_start_within_a_chunk(M, D, tx, td):
+    _bwd(_rows(M, D, tx), _rows(M, D, td, seed=5), _affine(D, F16)[0])
+
+
+def test_layer_norm_bwd_equal_shifts_and_untouched_padding():
+    # x, dy and dx start three elements behind a chunk's boundary, rows 2 elements apart.
+    M, D, ld = 61, 515, 517
+    x, dy = _rows(M, D, BF16, 2, 3), _rows(M, D, F32, 2, 3, seed=5)
+    w, b = _affine(D, F32)
+    _, mean, rstd = tw.layer_norm(x, w, b, stats=True)
+    ref = tw.layer_norm_bwd(dy, x, mean, rstd, w)
+    buf = torch.full((3 + M * ld,), 5.0, device="cuda", dtype=BF16)
+    dw, db = torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    size = tw.lib().twell_layer_norm_bwd_scratch_bytes(M, D)
+    scratch = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert tw.lib().twell_layer_norm_bwd(
+        dy.data_ptr(), 0, ld, x.data_ptr(), 1, ld, mean.data_ptr(), rstd.data_ptr(), w.data_ptr(), 0, M, D,
+        buf.data_ptr() + 6, ld, dw.data_ptr(), db.data_ptr(), scratch.data_ptr(), size,
+        torch.cuda.current_stream().cuda_stream) == tw.OK
+    dx = buf[3:].view(M, ld)
+    assert bool((buf[:3] == 5).all()) and bool((dx[:, D:] == 5).all())
+    # Both are within the bounds of _bwd of the formula; sums in other orders differ by no more than twice those.
+    for got, want in ((dx[:, :D], ref[0]), (dw, ref[1]), (db, ref[2])):
+        assert torch.allclose(got.float(), want.float(), rtol=2 ** -7, atol=1e-4)
+
+
 @pytest.mark.parametrize("gap,offset", [(1, 0), (8, 0), (8, 3)])
 def test_layer_norm_bwd_strides(gap, offset):
     _bwd(_rows(50, 520, BF16, gap, offset), _rows(50, 520, F32, gap, offset, seed=5), _affine(520, BF16)[0])
