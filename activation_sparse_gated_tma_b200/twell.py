@@ -434,6 +434,16 @@ def _matrix(M: int, N: int, dtype, like: torch.Tensor) -> torch.Tensor:
     return like.new_empty((M, N), dtype=dtype)
 
 
+def _rows_like(x: torch.Tensor, dtype) -> torch.Tensor:
+    """Contiguous, of x's shape (empty_like takes half a microsecond less than new_empty)."""
+    return torch.empty_like(x) if dtype is x.dtype and x.is_contiguous() else x.new_empty(x.shape, dtype=dtype)
+
+
+def _two_vectors(n: int, like: torch.Tensor):
+    a = like.new_empty(n, dtype=torch.float32)
+    return a, torch.empty_like(a)
+
+
 def _int8_rows(M: int, K: int, like: torch.Tensor):
     """int8 [M][K] whose row stride is a multiple of 16, as the products need it."""
     ld = -(-K // 16) * 16
@@ -462,10 +472,10 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         with _there(stream, x):
             return layer_norm(x, weight, bias, eps, out, out_dtype, stats)
     if out is None:
-        out, ldy = _matrix(M, D, out_dtype or x.dtype, x), D
+        out, ldy = _rows_like(x, out_dtype or x.dtype), D
     mean = rstd = pm = pr = None
     if stats:
-        mean, rstd = _matrix(2, M, torch.float32, x).unbind()
+        mean, rstd = _two_vectors(M, x)
         pm, pr = mean.data_ptr(), rstd.data_ptr()
     _check(lib().twell_layer_norm_fwd(x.data_ptr(), _DTYPES[x.dtype], ldx, w, b, wt, M, D, eps, out.data_ptr(),
                                       _DTYPES[out.dtype], ldy, pm, pr, _here(x)), "twell_layer_norm_fwd")
@@ -507,15 +517,15 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: 
         with _there(stream, x):
             return layer_norm_bwd(dy, x, mean, rstd, weight, param_grads, scratch)
     L = lib()
-    dx = _matrix(M, D, x.dtype, x)
+    dx = _rows_like(x, x.dtype)
     dw = db = pw = pb = ps = None
     size = 0
     if param_grads:
-        dw, db = _matrix(2, D, torch.float32, x).unbind()
+        dw, db = _two_vectors(D, x)
         pw, pb = dw.data_ptr(), db.data_ptr()
         if scratch is None:
             size = L.twell_layer_norm_bwd_scratch_bytes(M, D)
-            scratch = x.new_empty(size, dtype=torch.uint8)
+            scratch = dw.new_empty(size // 4)
         else:
             size = scratch.numel() * scratch.element_size()
         ps = scratch.data_ptr()
