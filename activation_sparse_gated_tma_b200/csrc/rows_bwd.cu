@@ -34,7 +34,11 @@ __global__ void __launch_bounds__(32 * kReduceWarps)
 }
 
 // Chunks a thread owns: the fewest of 1, 2, 4 with which kBwdThreads threads
-// own a row; two rows at a time where one chunk (of rows not read by elements)
+// own a row (8 is none).
+int bwd_chunks(int columns) {
+  return columns <= 8 * kBwdThreads ? 1 : columns <= 16 * kBwdThreads ? 2 : columns <= 32 * kBwdThreads ? 4 : 8;
+}
+// Two rows at a time where one chunk (of rows not read by elements)
 // leaves the registers for it.
 struct BwdShape {
   int chunks, warps, groups, rows, grid;
@@ -42,7 +46,7 @@ struct BwdShape {
 BwdShape bwd_shape(int M, int D, BwdRows kind, int classes, int sms) {
   BwdShape r;
   const int columns = kind == kShifted ? D + 7 : D;
-  r.chunks = columns <= 8 * kBwdThreads ? 1 : columns <= 16 * kBwdThreads ? 2 : 4;
+  r.chunks = bwd_chunks(columns);
   r.warps = (columns + 256 * r.chunks - 1) / (256 * r.chunks);
   r.rows = r.chunks == 1 && kind != kElements && 2 * 32 * r.warps * bwd_registers(1, 2, kind == kShifted) <= 65536 ? 2 : 1;
   // As many groups as an SM's registers take, in as few blocks as hold them: each block leaves a partial row.
@@ -80,8 +84,12 @@ void (*bwd_kernel(int chunks, int rows))(const LayerNormBwdParams, const BwdPlan
 template <class TX, class TDY>
 cudaError_t norm_bwd(const LayerNormBwdParams& p, bool aligned, int sms, int& parts, cudaStream_t s) {
   const int x0 = shift_of(p.x, p.x_type);
-  const bool shifted = !aligned && shift_of(p.dx, p.x_type) == x0 && shift_of(p.dy, p.dy_type) == x0 &&
-                       p.lddx % 8 == p.ldx % 8 && p.lddy % 8 == p.ldx % 8 && p.D + 7 <= 32 * kBwdThreads;
+  // (With few rows those at the matrix's ends, read by elements, hold up the others: bf16 16 x 2047 7.0 us, by elements
+  // 5.3; 300 x 1535 9.3 and 8.1, 1000 x 1535 11.4 and 13.5.  Where the shift takes a chunk more it does not pay:
+  // fp32 8191 x 4093 102 us, by elements 90.)
+  const bool shifted = !aligned && p.M > 4 * sms && bwd_chunks(p.D + 7) == bwd_chunks(p.D) &&
+                       shift_of(p.dx, p.x_type) == x0 && shift_of(p.dy, p.dy_type) == x0 && p.lddx % 8 == p.ldx % 8 &&
+                       p.lddy % 8 == p.ldx % 8;
   const BwdRows kind = aligned ? kAligned : shifted ? kShifted : kElements;
   const int classes = shifted ? shift_classes(p.ldx) : 1;
   const BwdShape r = bwd_shape(p.M, p.D, kind, classes, sms);
@@ -106,7 +114,7 @@ int layer_norm_bwd_max_parts(int M, int D, int sms) {
   int most = bwd_shape(M, D, kAligned, 1, sms).grid;
   const int elements = bwd_shape(M, D, kElements, 1, sms).grid;
   if (elements > most) most = elements;
-  if (D + 7 <= 32 * kBwdThreads)
+  if (bwd_chunks(D + 7) == bwd_chunks(D))
     for (int classes = 1; classes <= 8; classes *= 2) {
       const int shifted = bwd_shape(M, D, kShifted, classes, sms).grid;
       if (shifted > most) most = shifted;

@@ -145,15 +145,16 @@ def test_layer_norm_bwd(M, D, tx, td):
 
 
 @pytest.mark.parametrize("M,D,tx,td", [(4099, 2047, F16, F16), (1030, 1535, BF16, F32), (1, 9, F32, F32), (7, 2049, F32, BF16),
-                                       (40, 4089, BF16, BF16), (40, 4090, F32, F32), (17, 8188, F16, F32), (6, 16377, F32, F32),
-                                       (300, 12, BF16, BF16), (2000, 514, F32, F32), (11, 16378, BF16, F32)])
+                                       (600, 4089, BF16, BF16), (600, 4090, F32, F32), (640, 8188, F16, F32), (601, 16377, F32, F32),
+                                       (1300, 12, BF16, BF16), (2000, 514, F32, F32), (11, 16378, BF16, F32), (900, 1, F32, F32),
+                                       (777, 7, BF16, F32), (700, 4100, F16, F16)])
 def test_layer_norm_bwd_rows_that_start_within_a_chunk(M, D, tx, td):
     _bwd(_rows(M, D, tx), _rows(M, D, td, seed=5), _affine(D, F16)[0])
 
 
 def test_layer_norm_bwd_equal_shifts_and_untouched_padding():
     # x, dy and dx start three elements behind a chunk's boundary, rows 2 elements apart.
-    M, D, ld = 61, 515, 517
+    M, D, ld = 661, 515, 517
     x, dy = _rows(M, D, BF16, 2, 3), _rows(M, D, F32, 2, 3, seed=5)
     w, b = _affine(D, F32)
     _, mean, rstd = tw.layer_norm(x, w, b, stats=True)
