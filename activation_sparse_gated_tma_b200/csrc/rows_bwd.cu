@@ -43,14 +43,16 @@ int bwd_chunks(int columns) {
 struct BwdShape {
   int chunks, warps, groups, rows, grid;
 };
+// Warps whose registers an SM holds: each of its four parts has 16384 for every fourth warp.
+constexpr int resident_warps(int registers) { return 4 * (16384 / (32 * registers)); }
 BwdShape bwd_shape(int M, int D, BwdRows kind, int classes, int sms) {
   BwdShape r;
   const int columns = kind == kShifted ? D + 7 : D;
   r.chunks = bwd_chunks(columns);
   r.warps = (columns + 256 * r.chunks - 1) / (256 * r.chunks);
-  r.rows = r.chunks == 1 && kind != kElements && 2 * 32 * r.warps * bwd_registers(1, 2, kind == kShifted) <= 65536 ? 2 : 1;
+  r.rows = r.chunks == 1 && kind != kElements && 2 * r.warps <= resident_warps(bwd_registers(1, 2, kind == kShifted)) ? 2 : 1;
   // As many groups as an SM's registers take, in as few blocks as hold them: each block leaves a partial row.
-  const int fit = 65536 / (32 * bwd_registers(r.chunks, r.rows, kind == kShifted)) / r.warps;
+  const int fit = resident_warps(bwd_registers(r.chunks, r.rows, kind == kShifted)) / r.warps;
   int per_sm = 1;
   r.groups = 1;
   for (int blocks = 1; blocks <= 4; ++blocks) {

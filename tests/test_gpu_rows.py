@@ -152,6 +152,13 @@ def test_layer_norm_bwd_rows_that_start_within_a_chunk(M, D, tx, td):
     _bwd(_rows(M, D, tx), _rows(M, D, td, seed=5), _affine(D, F16)[0])
 
 
+@pytest.mark.parametrize("warps", range(1, 17))
+def test_layer_norm_bwd_every_number_of_warps_a_row(warps):
+    # Rows enough to fill every SM, aligned, shifted and by elements: every shape of block.
+    for D, gap in ((256 * warps, 0), (256 * warps - 9, 0), (256 * warps - 1, 1)):
+        _bwd(_rows(3000, D, BF16, gap), _rows(3000, D, F32, seed=5), None)
+
+
 def test_layer_norm_bwd_equal_shifts_and_untouched_padding():
     # x, dy and dx start three elements behind a chunk's boundary, rows 2 elements apart.
     M, D, ld = 661, 515, 517
