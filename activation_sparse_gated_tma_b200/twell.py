@@ -447,8 +447,9 @@ def _two_vectors(n: int, like: torch.Tensor):
 def _int8_rows(M: int, K: int, like: torch.Tensor):
     """int8 [M][K] whose row stride is a multiple of 16, as the products need it."""
     ld = -(-K // 16) * 16
-    q = _matrix(M, ld, torch.int8, like)
-    return (q if ld == K else q[:, :K]), ld
+    if ld == K:
+        return _matrix(M, K, torch.int8, like), ld
+    return like.new_empty_strided((M, K), (ld, 1), dtype=torch.int8), ld
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
