@@ -49,8 +49,8 @@ __device__ __forceinline__ void store4_y(TY* y, const float (&v)[4], int inside,
   }
 }
 
-// u * ReLU(g); a NaN in g (a token or channel without a scale) stays one.
-__device__ __forceinline__ float gated_value(float g, float u) { return g <= 0.f ? 0.f : g * u; }
+// u * ReLU(g); a NaN in g or u (a token or channel without a scale) stays one.
+__device__ __forceinline__ float gated_value(float g, float u) { return (g <= 0.f ? 0.f : g) * u; }
 
 // ---------------------------------------------------------------------------
 // One tile per CTA (128 channels x BT tokens, two accumulators when GATED); a

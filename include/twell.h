@@ -361,8 +361,9 @@ twell_status twell_int8_linear(const int8_t* x, int64_t ldx, const float* x_scal
 
 /*
  * The gated pair of such products of the same tokens, h = u ReLU(g) with
- * g = x wg^T and u = x wu^T scaled as above (h is 0 where g <= 0; NaN scales
- * give NaN): the first stage of the dense FFN (dense_ffn_fwd) on int8 weights.
+ * g = x wg^T and u = x wu^T scaled as above (h is 0 where g <= 0 and u is
+ * finite; a NaN scale of the token, the gate's or the up channel gives NaN):
+ * the first stage of the dense FFN (dense_ffn_fwd) on int8 weights.
  */
 twell_status twell_int8_gated(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* wg, int64_t ldwg,
                               const float* wg_scale, const int8_t* wu, int64_t ldwu, const float* wu_scale, int M, int N,
