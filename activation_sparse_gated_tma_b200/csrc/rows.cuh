@@ -504,8 +504,9 @@ __device__ __forceinline__ void store_row_i8(int8_t* row, int D, int t, int nt, 
 // y = (x - mu) r w + b.  The variance is taken from the deviations (two
 // reductions over registers, no second read): sums of squares would cancel for
 // rows whose mean is far above their spread (as x r - mu r would, where x - mu is
-// exact).  TO int8_t: y is quantised from its fp32 values, with one more
-// reduction for the row's largest magnitude.
+// exact); of such rows the mean is corrected by the deviations' own.  TO int8_t:
+// y is quantised from its fp32 values, with one more reduction for the row's
+// largest magnitude.
 // The weight and the bias are staged in shared memory once per block (from
 // global memory every row's reads cost 4 us at bf16 16384 x 2560), each layer's first and
 // second halves of chunks apart, so that the lanes' 16-byte reads meet
@@ -542,18 +543,37 @@ __global__ void __launch_bounds__(kRowThreads, norm_blocks(NC))
     for (int j = 0; j < NC; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i & 3] += v[j].e[i];
-    const float mean = group_sum(g, (s[0] + s[1]) + (s[2] + s[3])) * p.inv_d;
-    s[0] = s[1] = s[2] = s[3] = 0.f;
+    float mean = group_sum(g, (s[0] + s[1]) + (s[2] + s[3])) * p.inv_d;
+    auto take_off = [&](float d) {
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const int c = 8 * (g.t + j * g.nt);
+      for (int j = 0; j < NC; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[j].e[i] -= mean;
-        if (j < full_layers(NC) || c + (ALIGNED ? 0 : i) < p.D) s[i & 3] = fmaf(v[j].e[i], v[j].e[i], s[i & 3]);
+        for (int i = 0; i < 8; ++i) v[j].e[i] -= d;
+    };
+    // Sum over the row of f(deviation) added up in turn (behind the row they are 0 - mean).
+    auto sum_of = [&](auto f) {
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int c = 8 * (g.t + j * g.nt);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (j < full_layers(NC) || c + (ALIGNED ? 0 : i) < p.D) s[i & 3] = f(s[i & 3], v[j].e[i]);
       }
+      return group_sum(g, (s[0] + s[1]) + (s[2] + s[3]));
+    };
+    auto plus_square = [](float s, float d) { return fmaf(d, d, s); };
+    take_off(mean);
+    float rstd = rsqrtf(sum_of(plus_square) * p.inv_d + p.eps);
+    // This mean is off by a few 2^-24 of itself: where it is far above the spread, by much of a deviation (or so much
+    // that the squares pass the range and leave no rstd).  The deviations' own mean, off by as little of itself, takes
+    // that off again.  The whole group does or does not; other rows do not pay for the two more sums.
+    if (fabsf(mean) * rstd > 4.f || rstd == 0.f) {
+      const float off = sum_of([](float s, float d) { return s + d; }) / static_cast<float>(p.D);
+      mean += off;
+      take_off(off);
+      rstd = rsqrtf(sum_of(plus_square) * p.inv_d + p.eps);
     }
-    const float rstd = rsqrtf(group_sum(g, (s[0] + s[1]) + (s[2] + s[3])) * p.inv_d + p.eps);
     auto result = [&](int j) {
       const float* w = vectors + 8 * j * g.nt + 4 * g.t;
       const float4 wa = *reinterpret_cast<const float4*>(w), wb = *reinterpret_cast<const float4*>(w + 4 * g.nt);

@@ -296,7 +296,8 @@ typedef enum { TWELL_F32 = 0, TWELL_BF16 = 1, TWELL_F16 = 2, TWELL_I8 = 3 } twel
  *   mean = sum x / D, rstd = 1 / sqrt(sum (x - mean)^2 / D + eps),
  *   y = (x - mean) rstd weight + bias.
  * weight, bias [D] of w_type (F32, BF16, F16), or NULL for ones and zeros;
- * mean, rstd [M] fp32 outputs, or NULL.  All arithmetic is fp32; y is rounded
+ * mean, rstd [M] fp32 outputs, or NULL.  All arithmetic is fp32 (a mean above
+ * four times the spread is corrected by the mean of x - mean); y is rounded
  * once.  y_type is x_type, or F32, or (x_type F32) any floating type.  The FFN's
  * rows with the gate bias in column K-1 are the outputs of D = K-1, ldy = K (that
  * column is then left alone), or of D = K with weight[K-1] = 0, bias[K-1] = 1.

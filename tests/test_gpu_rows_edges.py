@@ -1,0 +1,49 @@
+"""Rows at the edges of the row kernels' arithmetic and launches: lanes behind a
+row, means far above the spread, calls from two host threads, many rows.
+
+u = 2^-24 is fp32's half step; a row sum of terms t is within 64 u sum|t| (see
+test_gpu_rows.py, whose helpers and bounds these tests share)."""
+import threading
+
+import pytest
+import torch
+
+from activation_sparse_gated_tma_b200 import twell as tw
+from tests.test_gpu_rows import BF16, EPS, F16, F32, U, _affine, _bwd, _check_norm, _half_step, _norm64, _quant64, _rows
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- means far above the spread
+@pytest.mark.parametrize("D", [1000, 4093, 2047, 1535, 4096])
+@pytest.mark.parametrize("dtype,value", [(BF16, 6016.0), (BF16, 8064.0), (F16, 6016.0), (F32, 1234.567), (F32, -3e7)])
+def test_layer_norm_of_constant_rows_is_the_bias(D, dtype, value):
+    x = _rows(7, D, dtype)
+    x[2] = value
+    w, b = _affine(D, F32)
+    y, mean, _ = tw.layer_norm(x, w, b, EPS, out_dtype=F32, stats=True)
+    assert torch.equal(y[2], b) and float(mean[2]) == float(x[2, 0])
+    q, scale = tw.layer_norm_int8(x, w, b, EPS)
+    ref, s = _quant64(b[None])
+    assert torch.equal(q[2].double(), ref[0]) and float(scale[2]) == float(s[0])
+
+
+@pytest.mark.parametrize("M,D", [(5, 2560), (300, 1000), (3, 2047), (4, 8192), (9, 16383), (700, 300)])
+@pytest.mark.parametrize("level,spread", [(1000.0, 0.01), (-3e5, 2.0), (20.0, 1.0)])
+def test_layer_norm_of_rows_far_from_zero(M, D, level, spread):
+    # The deviations that count are those from the row's true mean.  A first mean is within 64 u |mean| of it, so the
+    # deviations from that one are below |x - mean| + 64 u |mean|; their sum, and with it the correction, is within
+    # 64 u of their magnitudes' sum, and each deviation adds its own rounding.  Rows whose mean is up to four times
+    # the spread (4.1 with what both are off by) need no correction: there the first mean's 64 u |mean| counts.
+    x = (_rows(M, D, F32) * spread + level).contiguous()
+    w, b = _affine(D, F32)
+    y, mean, rstd = tw.layer_norm(x, w, b, 0.0, stats=True)
+    ref, m64, r64, hat = _norm64(x, w, b, 0.0)
+    off = (x.double() - m64).abs().mean(1, keepdim=True) + 64 * U * m64.abs()
+    off += torch.where(m64.abs() * r64 <= 4.1, m64.abs(), 0.0)
+    wa, ba = w.double().abs(), b.double().abs()
+    tol = _half_step(F32, ref) + 64 * U * (wa * (hat.abs() + r64 * off) + ba) * (1 + 64 * U)
+    err = (y.double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    assert bool(((mean.double()[:, None] - m64).abs() <= U * m64.abs() + 64 * U * off * (1 + U)).all())
+    assert bool(((rstd.double()[:, None] - r64).abs() <= 64 * U * r64 * (1 + (64 * U * off * r64) ** 2 / U)).all())
