@@ -542,8 +542,11 @@ __global__ void __launch_bounds__(kRowThreads, norm_blocks(NC))
 #pragma unroll
     for (int j = 0; j < NC; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i & 3] += v[j].e[i];
-    float mean = group_sum(g, (s[0] + s[1]) + (s[2] + s[3])) * p.inv_d;
+      for (int i = 0; i < 8; ++i) s[i & 3] = fmaf(v[j].e[i], 0x1p-15f, s[i & 3]);
+    // (Of at most 2^14 elements at 2^-15 the sum stays within the range.  Rounding may still take the mean of rows of
+    // the largest value out of it.)
+    float mean = group_sum(g, (s[0] + s[1]) + (s[2] + s[3])) * (p.inv_d * 0x1p15f);
+    if (fabsf(mean) > 3.402823466e38f) mean = copysignf(3.402823466e38f, mean);
     auto take_off = [&](float d) {
 #pragma unroll
       for (int j = 0; j < NC; ++j)

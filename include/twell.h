@@ -297,8 +297,9 @@ typedef enum { TWELL_F32 = 0, TWELL_BF16 = 1, TWELL_F16 = 2, TWELL_I8 = 3 } twel
  *   y = (x - mean) rstd weight + bias.
  * weight, bias [D] of w_type (F32, BF16, F16), or NULL for ones and zeros;
  * mean, rstd [M] fp32 outputs, or NULL.  All arithmetic is fp32 (a mean above
- * four times the spread is corrected by the mean of x - mean); y is rounded
- * once.  y_type is x_type, or F32, or (x_type F32) any floating type.  The FFN's
+ * four times the spread is corrected by the mean of x - mean, and a row's sum
+ * may pass the fp32 range; rows of finite values whose squared deviations pass
+ * it have rstd 0 and give the bias); y is rounded once.  y_type is x_type, or F32, or (x_type F32) any floating type.  The FFN's
  * rows with the gate bias in column K-1 are the outputs of D = K-1, ldy = K (that
  * column is then left alone), or of D = K with weight[K-1] = 0, bias[K-1] = 1.
  */

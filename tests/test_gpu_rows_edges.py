@@ -47,3 +47,16 @@ def test_layer_norm_of_rows_far_from_zero(M, D, level, spread):
     assert bool((err <= tol).all()), float((err / tol).max())
     assert bool(((mean.double()[:, None] - m64).abs() <= U * m64.abs() + 64 * U * off * (1 + U)).all())
     assert bool(((rstd.double()[:, None] - r64).abs() <= 64 * U * r64 * (1 + (64 * U * off * r64) ** 2 / U)).all())
+
+
+@pytest.mark.parametrize("D", [2, 64, 1000, 2560, 4093, 8192, 16383, 16384])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_layer_norm_of_rows_whose_sum_passes_the_range(D, dtype):
+    x = _rows(6, D, dtype)
+    x[1], x[3], x[4] = 3e38, -torch.finfo(dtype).max, torch.finfo(dtype).max
+    w, b = _affine(D, F32)
+    y, mean, rstd = tw.layer_norm(x, w, b, EPS, out_dtype=F32, stats=True)
+    for r in (1, 3, 4):
+        assert torch.equal(y[r], b) and float(mean[r]) == float(x[r, 0])
+        assert abs(float(rstd[r]) * EPS ** 0.5 - 1) <= 8 * U
+    _check_norm(y[::5], mean[::5], rstd[::5], x[::5], w, b)
