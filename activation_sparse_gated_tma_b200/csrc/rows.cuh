@@ -594,8 +594,11 @@ __global__ void __launch_bounds__(kRowThreads, norm_blocks(NC))
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         v[j] = result(j);
-        // Behind the row the weight and the bias are 0, unless the row has no finite mean.
-        m = max_abs(m, v[j]);
+        const int c = 8 * (g.t + j * g.nt);
+        // Behind the row (0 - mean) rstd may pass the fp32 range, which the weight of 0 there makes a NaN.
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (j < full_layers(NC) || c + (ALIGNED ? 0 : i) < p.D) m = max_abs(m, v[j].e[i]);
       }
       const RowScale r = row_scale<false>(group_max(g, m));
       store_row_i8<NC, ALIGNED, false>(y, p.D, g.t, g.nt, r, [&](int j) { return v[j]; });

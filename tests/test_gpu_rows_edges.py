@@ -14,6 +14,23 @@ from tests.test_gpu_rows import BF16, EPS, F16, F32, U, _affine, _bwd, _check_no
 pytestmark = pytest.mark.gpu
 
 
+# ---------------------------------------------------------------- lanes behind a row
+@pytest.mark.parametrize("D", [64, 63, 33, 96, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_layer_norm_int8_of_large_constant_rows(D, dtype):
+    # (0 - mean) rstd passes the fp32 range, the rows' own deviations are 0: y is the bias.
+    x = _rows(5, D, dtype)
+    x[1], x[3] = 2.0 ** 120, -2.0 ** 121
+    w, b = _affine(D, F32)
+    y = tw.layer_norm(x, w, b, EPS, out_dtype=F32)
+    assert torch.equal(y[1], b) and torch.equal(y[3], b)
+    q, scale = tw.layer_norm_int8(x, w, b, EPS)
+    ref, s = _quant64(y)
+    for r in (1, 3):
+        assert float(scale[r]) == float(s[r]) and torch.equal(q[r].double(), ref[r])
+    assert bool(scale.isfinite().all())
+
+
 # ---------------------------------------------------------------- means far above the spread
 @pytest.mark.parametrize("D", [1000, 4093, 2047, 1535, 4096])
 @pytest.mark.parametrize("dtype,value", [(BF16, 6016.0), (BF16, 8064.0), (F16, 6016.0), (F32, 1234.567), (F32, -3e7)])
@@ -56,7 +73,10 @@ def test_layer_norm_of_rows_whose_sum_passes_the_range(D, dtype):
     x[1], x[3], x[4] = 3e38, -torch.finfo(dtype).max, torch.finfo(dtype).max
     w, b = _affine(D, F32)
     y, mean, rstd = tw.layer_norm(x, w, b, EPS, out_dtype=F32, stats=True)
+    q, scale = tw.layer_norm_int8(x, w, b, EPS)
+    ref, s = _quant64(b[None])
     for r in (1, 3, 4):
         assert torch.equal(y[r], b) and float(mean[r]) == float(x[r, 0])
         assert abs(float(rstd[r]) * EPS ** 0.5 - 1) <= 8 * U
+        assert torch.equal(q[r].double(), ref[0]) and float(scale[r]) == float(s[0])
     _check_norm(y[::5], mean[::5], rstd[::5], x[::5], w, b)
