@@ -214,7 +214,9 @@ __global__ void __maxnreg__(bwd_registers(NC, R, ROWS == kShifted))
         }
       }
     }
-    // Outside the row dy is 0, so x's value there adds nothing.
+    // Outside the row x and dy are 0, so nothing is added there: 0 times 0 - mean.  (The sum of g xh takes its rstd
+    // afterwards.  (0 - mean) rstd may pass the fp32 range where all of the row is far from zero, and 0 times that is
+    // NaN; so may the sum before rstd where the squared deviations did and left an rstd of 0.)
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float a[2] = {0.f, 0.f}, b[2] = {0.f, 0.f};
@@ -223,15 +225,15 @@ __global__ void __maxnreg__(bwd_registers(NC, R, ROWS == kShifted))
         const Oct xv = unpack8(x[r][j]), dv = unpack8(dy[r][j]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float xh = (xv.e[i] - mean[r]) * rstd[r], gr = dv.e[i] * w[j].e[i];
-          dw[j].e[i] = fmaf(dv.e[i], xh, dw[j].e[i]);
+          const float off = xv.e[i] - mean[r], gr = dv.e[i] * w[j].e[i];
+          dw[j].e[i] = fmaf(dv.e[i], off * rstd[r], dw[j].e[i]);
           db[j].e[i] += dv.e[i];
           a[i & 1] += gr;
-          b[i & 1] = fmaf(gr, xh, b[i & 1]);
+          b[i & 1] = fmaf(gr, off, b[i & 1]);
         }
       }
       sum[2 * r] = a[0] + a[1];
-      sum[2 * r + 1] = b[0] + b[1];
+      sum[2 * r + 1] = rstd[r] == 0.f ? 0.f : (b[0] + b[1]) * rstd[r];
     }
     group_sums<R>(g, flip, sh, sum);
     flip ^= 1;

@@ -80,3 +80,39 @@ def test_layer_norm_of_rows_whose_sum_passes_the_range(D, dtype):
         assert abs(float(rstd[r]) * EPS ** 0.5 - 1) <= 8 * U
         assert torch.equal(q[r].double(), ref[0]) and float(scale[r]) == float(s[0])
     _check_norm(y[::5], mean[::5], rstd[::5], x[::5], w, b)
+
+
+@pytest.mark.parametrize("D", [64, 63, 33, 1000, 2040, 2047, 4100, 4097])
+@pytest.mark.parametrize("M", [7, 1300])
+@pytest.mark.parametrize("tx,td", [(F32, F32), (BF16, BF16)])
+def test_layer_norm_bwd_of_large_constant_rows(M, D, tx, td):
+    # mean rstd passes the fp32 range (2^110 10^6) while x - mean is 0: dx is rstd (g - sum g / D).
+    x, dy = _rows(M, D, tx), _rows(M, D, td, seed=5)
+    w = _affine(D, F32)[0]
+    x[1::3] = 2.0 ** 110
+    mean, rstd = x.double().mean(1).float(), torch.ones(M, device="cuda")
+    mean[1::3], rstd[1::3] = 2.0 ** 110, 1e6
+    dx, dw, db = tw.layer_norm_bwd(dy, x, mean, rstd, w)
+    d, m, r = dy.double(), mean.double()[:, None], rstd.double()[:, None]
+    hat = (x.double() - m) * r
+    gr = d * w.double()
+    ref = r * (gr - gr.mean(1, keepdim=True) - hat * (gr * hat).mean(1, keepdim=True))
+    tol = _half_step(tx, ref) + 64 * U * r * (
+        gr.abs() + gr.abs().mean(1, keepdim=True) + hat.abs() * (gr * hat).abs().mean(1, keepdim=True)) * (
+            1 + torch.finfo(tx).eps)
+    assert bool(((dx.double() - ref).abs() <= tol).all())
+    for got, terms in ((dw, d * hat), (db, d)):
+        assert bool(((got.double() - terms.sum(0)).abs() <= 128 * U * terms.abs().sum(0)).all())
+
+
+def test_layer_norm_bwd_of_rows_without_rstd():
+    # Squared deviations past the fp32 range leave rstd 0, and with it dx.
+    x, dy = _rows(9, 1000, F32), _rows(9, 1000, F32, seed=5)
+    x[4] *= 1e37
+    _, mean, rstd = tw.layer_norm(x, stats=True)
+    assert float(rstd[4]) == 0
+    dx, dw, db = tw.layer_norm_bwd(dy, x, mean, rstd)
+    assert not dx[4].any() and bool(dx.isfinite().all())
+    keep = torch.arange(9, device="cuda") != 4
+    _bwd(x[keep], dy[keep], None)
+    assert bool(dw.isfinite().all()) and bool(db.isfinite().all())
