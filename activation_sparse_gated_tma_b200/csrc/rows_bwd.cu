@@ -104,7 +104,9 @@ cudaError_t norm_bwd(const LayerNormBwdParams& p, bool aligned, int sms, int& pa
                                        : bwd_kernel<TX, TDY, kElements>(r.chunks, r.rows);
   const size_t smem = r.groups > 1 ? static_cast<size_t>(r.groups) * 2 * p.D * sizeof(float) : 0;
   if (smem > 40 * 1024) {  // up to 48 KB with the static part, no attribute is needed
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // groups * warps fit an SM, and a row has at most 256 columns a warp and chunk
+    const int most = 2 * 256 * r.chunks * resident_warps(bwd_registers(r.chunks, r.rows, kind == kShifted)) * sizeof(float);
+    const cudaError_t e = allow_shared(kern, most);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(kern, r.grid, 32 * r.warps * r.groups, smem, s, p, plan);

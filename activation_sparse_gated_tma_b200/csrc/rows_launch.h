@@ -25,6 +25,14 @@ inline void rows_inside(const void* p, int64_t ld, int M, int D, int type, uint3
   while (begin < end && ((base + (end - 1) * step + bytes + piece - 1) & ~(piece - 1)) > last) --end;
 }
 
+// A kernel's limit of dynamic shared memory: `most` is the most that any call of
+// it takes, not what this one does.  The limit belongs to the kernel, and a lower
+// one set by another host thread before this one's launch would refuse the launch.
+template <class Kernel>
+cudaError_t allow_shared(Kernel kern, int most) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 // Warps per row, chunks per thread, rows (groups) per block.
 struct RowShape {
   int warps, chunks, groups;

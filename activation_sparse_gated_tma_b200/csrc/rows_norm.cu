@@ -17,11 +17,11 @@ cudaError_t norm(const LayerNormParams& p, bool aligned, int sms, cudaStream_t s
   switch (r.chunks) { TW_NC(1) TW_NC(2) TW_NC(3) TW_NC(4) TW_NC(5) TW_NC(6) TW_NC(8) TW_NC(10) }
 #undef TW_NC
   // Weight and bias, 227 KB at most per SM.
-  const int vectors = 2 * 4 * 8 * r.chunks * 32 * r.warps;
+  const int each = 2 * 4 * 8 * r.chunks * 32, vectors = each * r.warps;
   int per_sm = norm_blocks(r.chunks);
   while (per_sm > 1 && per_sm * (kRowThreads / r.threads()) * (vectors + 2048) > 220 * 1024) --per_sm;
   if (vectors > 40 * 1024) {  // up to 48 KB with the static part, no attribute is needed
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, vectors);
+    const cudaError_t e = allow_shared(kern, each * kMaxGroupWarps);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(kern, row_grid(p.M, r, per_sm, sms), r.threads(), vectors, s, p, plan);

@@ -116,3 +116,68 @@ def test_layer_norm_bwd_of_rows_without_rstd():
     keep = torch.arange(9, device="cuda") != 4
     _bwd(x[keep], dy[keep], None)
     assert bool(dw.isfinite().all()) and bool(db.isfinite().all())
+
+
+# ---------------------------------------------------------------- host threads
+def _in_threads(calls, times):
+    """Each (library function, arguments before the stream) in two threads of its
+    own, on streams of their own: the calls overlap in the library."""
+    statuses = []
+
+    def loop(function, args):
+        s = torch.cuda.Stream()
+        args = (*args, s.cuda_stream)
+        bad = [st for st in (function(*args) for _ in range(times)) if st != tw.OK]
+        s.synchronize()
+        statuses.append((len(bad), (tw.lib().twell_last_error() or b"").decode() if bad else ""))
+    threads = [threading.Thread(target=loop, args=c) for c in calls for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(statuses) == len(threads) and not any(n for n, _ in statuses), statuses
+
+
+def test_threads_that_norm_rows_of_different_lengths():
+    # 16384 and 8192 columns are eight chunks a thread in one kernel, with 128 and 64 KB of shared memory.
+    keep = []
+
+    def call(D):
+        x = _rows(2, D, F32)
+        keep.append((x, torch.empty_like(x)))
+        return tw.lib().twell_layer_norm_fwd, (x.data_ptr(), 0, D, None, None, 0, 2, D, 1e-5, keep[-1][1].data_ptr(), 0,
+                                               D, None, None)
+    # (Two rows of 8192 columns would take more warps and fewer chunks: 300 of them do not.)
+    a = call(16384)
+    x, y = _rows(300, 8192, F32), torch.empty((300, 8192), device="cuda")
+    b = (tw.lib().twell_layer_norm_fwd, (x.data_ptr(), 0, 8192, None, None, 0, 300, 8192, 1e-5, y.data_ptr(), 0, 8192,
+                                         None, None))
+    torch.cuda.synchronize()
+    _in_threads([a, b], 10000)
+    torch.cuda.synchronize()
+    _check_norm(y, None, None, x, None, None)
+    _check_norm(keep[0][1], None, None, keep[0][0], None, None)
+
+
+@pytest.mark.parametrize("lengths", [(2048, 2816), (4096, 3200)])
+def test_threads_that_differentiate_rows_of_different_lengths(lengths):
+    # One kernel, 48 and 44 KB of sums (64 and 50).
+    keep = []
+
+    def call(D):
+        M = 900
+        x = _rows(M, D, F32)
+        _, mean, rstd = tw.layer_norm(x, stats=True)
+        dx = torch.empty_like(x)
+        keep.append((x, mean, rstd, dx))
+        size = tw.lib().twell_layer_norm_bwd_scratch_bytes(M, D)
+        scratch = torch.empty(size, dtype=torch.uint8, device="cuda")
+        dw = torch.empty(D, device="cuda")
+        keep.append((scratch, dw))
+        return tw.lib().twell_layer_norm_bwd, (x.data_ptr(), 0, D, x.data_ptr(), 0, D, mean.data_ptr(), rstd.data_ptr(),
+                                               None, 0, M, D, dx.data_ptr(), D, dw.data_ptr(), None, scratch.data_ptr(), size)
+    calls = [call(D) for D in lengths]
+    torch.cuda.synchronize()
+    _in_threads(calls, 5000)
+    for x, mean, rstd, dx in keep[::2]:   # (dw is left out: two threads use one scratch)
+        assert torch.equal(dx, tw.layer_norm_bwd(x, x, mean, rstd, param_grads=False)[0])
