@@ -39,26 +39,32 @@ double int8_cost(const Int8Plan& plan, int M, int N, int K, bool gated, bool ali
 
 }  // namespace
 
+// (Gated tiles of 128 tokens have no room to share a reduction.)
+bool int8_can_cut(const Int8Plan& plan, int K, bool gated, int sms) {
+  if (plan.pairs) return sms >= 2;
+  const int64_t kb = div_up(K, kI8BK);
+  return div_up(kb, div_up(kb, plan.k_splits)) == plan.k_splits && !(gated && plan.token_tile == 128 && plan.k_splits > 1);
+}
+
 // The cut with the least estimated time: CTA pairs, or tiles of 16 to 128
 // tokens (no more than hold the batch) with a reduction of 1 to 8 shares, none
-// of them empty.  (Gated tiles of 128 tokens have no room to share one.)
+// of them empty.
 Int8Plan int8_plan(int M, int N, int K, bool gated, bool aligned_rows, int sms) {
   Int8Plan best{false, 16, 1};
   double least = int8_cost(best, M, N, K, gated, aligned_rows, sms);
   auto consider = [&](const Int8Plan& plan) {
+    if (!int8_can_cut(plan, K, gated, sms)) return;
     const double t = int8_cost(plan, M, N, K, gated, aligned_rows, sms);
     if (t < least) {
       least = t;
       best = plan;
     }
   };
-  const int64_t kb = div_up(K, kI8BK);
   for (int tile = 16; tile <= 128; tile *= 2) {
     if (tile > 16 && tile / 2 >= M) break;
-    for (int s = 1; s <= 8; s *= 2)
-      if (div_up(kb, div_up(kb, s)) == s && !(gated && tile == 128 && s > 1)) consider(Int8Plan{false, tile, s});
+    for (int s = 1; s <= 8; s *= 2) consider(Int8Plan{false, tile, s});
   }
-  if (sms >= 2) consider(Int8Plan{true, 128, 1});
+  consider(Int8Plan{true, 128, 1});
   return best;
 }
 

@@ -32,6 +32,8 @@ struct Int8Plan {
   int token_tile;
   int k_splits;
 };
+// Whether a product can be cut as `plan` (no share of a reduction may be empty).
+bool int8_can_cut(const Int8Plan& plan, int K, bool gated, int sms);
 // aligned_rows: the output's rows start on 16 bytes.
 Int8Plan int8_plan(int M, int N, int K, bool gated, bool aligned_rows, int sms);
 // Rows of the boxes of the operands' tensor maps (all kI8BK wide).

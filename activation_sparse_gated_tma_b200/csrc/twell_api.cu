@@ -37,6 +37,8 @@ thread_local long long g_expire_wait_ns = 0;
 // Route of the slotted rows in twell_ffn_bwd on this thread
 // (twell_bwd_slot_route): 0 by cost, 1 the dense-slot GEMMs, 2 the gather passes.
 thread_local int g_bwd_slot_route = 0;
+// Cut of the int8 products on this thread (twell_int8_cut); a tile of 0: by estimated time.
+thread_local int g_int8_tile = 0, g_int8_splits = 1;
 
 // Optional launch tracing: events[2i] / events[2i+1] bracket the i-th kernel.
 struct Trace {
@@ -675,7 +677,11 @@ twell_status int8_product(const int8_t* x, int64_t ldx, const float* x_scale, co
   DeviceInfo dev;
   if ((st = device_info(dev)) != TWELL_OK) return st;
   const bool aligned_rows = aligned16(y) && (ldy * type_bytes(y_type)) % 16 == 0;
-  const Int8Plan plan = int8_plan(M, N, K, gated, aligned_rows, dev.sms);
+  Int8Plan plan{g_int8_tile == 256, g_int8_tile == 256 ? 128 : g_int8_tile, g_int8_splits};
+  if (g_int8_tile == 0)
+    plan = int8_plan(M, N, K, gated, aligned_rows, dev.sms);
+  else if (!int8_can_cut(plan, K, gated, dev.sms))
+    return fail(TWELL_ERR_INVALID, "K=%d cannot be cut into %d shares with tiles of %d tokens", K, g_int8_splits, g_int8_tile);
   CUtensorMap tm_x, tm_w, tm_w2;
   // (Encoded for every call, a fraction of a microsecond: activations move.)
   auto encode = [](const int8_t* q, int64_t ld, int rows, int cols, int box, CUtensorMap& out) {
@@ -727,6 +733,16 @@ twell_status twell_test_expire_wait(long long limit_ns) {
 twell_status twell_bwd_slot_route(int route) {
   if (route < 0 || route > 2) return fail(TWELL_ERR_INVALID, "route must be 0, 1 or 2, got %d", route);
   g_bwd_slot_route = route;
+  return TWELL_OK;
+}
+
+twell_status twell_int8_cut(int token_tile, int k_splits) {
+  const bool tile = token_tile == 16 || token_tile == 32 || token_tile == 64 || token_tile == 128;
+  const bool shares = k_splits == 1 || (tile && (k_splits == 2 || k_splits == 4 || k_splits == 8));
+  if (!(tile || token_tile == 0 || token_tile == 256) || !shares)
+    return fail(TWELL_ERR_INVALID, "no cut of %d tokens and %d shares", token_tile, k_splits);
+  g_int8_tile = token_tile;
+  g_int8_splits = k_splits;
   return TWELL_OK;
 }
 

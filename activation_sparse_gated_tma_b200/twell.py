@@ -76,6 +76,7 @@ def lib() -> ctypes.CDLL:
         "twell_dequantize_rows": (I, [P, LL, P, I, I, P, I, LL, P]),
         "twell_int8_linear": (I, [P, LL, P, P, LL, P, P, I, I, I, P, I, LL, P]),
         "twell_int8_gated": (I, [P, LL, P, P, LL, P, P, LL, P, I, I, I, P, I, LL, P]),
+        "twell_int8_cut": (I, [I, I]),
         "dense_ffn_fwd": (I, [P, P, P, P, I, I, I, P, P, P]),
         "dense_ffn_fwd_bf16h": (I, [P, P, P, P, I, I, I, P, P, P]),
         "dense_ffn_fwd_noalloc": (I, [P, P, P, P, I, I, I, P, P]),
@@ -619,6 +620,13 @@ def int8_gated(x: torch.Tensor, x_scale: torch.Tensor, wg: torch.Tensor, wg_scal
     _check(lib().twell_int8_gated(x.data_ptr(), ldx, xs, wg.data_ptr(), ldg, gs, wu.data_ptr(), ldu, us, M, N, K,
                                   h.data_ptr(), _DTYPES[h.dtype], ldh, _here(x)), "twell_int8_gated")
     return h
+
+
+def int8_cut(token_tile: int = 0, k_splits: int = 1) -> None:
+    """twell_int8_cut: how the following int8 products on this thread are cut;
+    0 chooses by estimated time, 256 CTA pairs, 16 to 128 tiles of that many
+    tokens with a reduction of k_splits shares (per thread)."""
+    _check(lib().twell_int8_cut(int(token_tile), int(k_splits)), "twell_int8_cut")
 
 
 class Int8FFN(NamedTuple):

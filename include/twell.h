@@ -372,6 +372,18 @@ twell_status twell_int8_gated(const int8_t* x, int64_t ldx, const float* x_scale
                               int K, void* h, twell_dtype h_type, int64_t ldh, cudaStream_t stream);
 
 /*
+ * Cut of the following int8 products on the calling thread: token_tile 0 (the
+ * default) by estimated time, 256 always on CTA pairs (256 x 256 tiles, k_splits
+ * 1), 16, 32, 64 or 128 always in tiles of 128 channels by that many tokens whose
+ * reduction k_splits CTAs (1, 2, 4 or 8) share.  The results do not depend on the
+ * cut but for the rounding of fp32 products fused with the bias.  Returns
+ * TWELL_ERR_INVALID for other values; a product that cannot be cut so (a share
+ * without a 128-wide block of K, or a gated tile of 128 tokens that is shared)
+ * returns it when called.
+ */
+twell_status twell_int8_cut(int token_tile, int k_splits);
+
+/*
  * Host-side fault injection for tests of the device status path.  Arms a
  * one-shot for the next twell_ffn_fwd on this thread: its fused kernel waits
  * for one more scanned token row than exist, a condition nothing makes true,

@@ -137,3 +137,11 @@ def test_python_wrapper_rejects_wrong_tensors():
     import torch
     with pytest.raises(ValueError):
         tw._bf16(torch.zeros(4, 4), "x", (4, 4))          # wrong dtype / not CUDA
+
+
+def test_int8_cut_validates_its_values():
+    L = tw.lib()
+    for bad in ((-1, 1), (8, 1), (48, 1), (512, 1), (16, 0), (16, 3), (16, 16), (256, 2), (0, 2)):
+        assert L.twell_int8_cut(*bad) == tw.ERR_INVALID, bad
+    for ok in ((16, 8), (128, 1), (256, 1), (0, 1)):  # ends on the default
+        assert L.twell_int8_cut(*ok) == tw.OK
