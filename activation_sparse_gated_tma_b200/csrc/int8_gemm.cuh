@@ -52,6 +52,21 @@ __device__ __forceinline__ void store4_y(TY* y, const float (&v)[4], int inside,
 // u * ReLU(g); a NaN in g or u (a token or channel without a scale) stays one.
 __device__ __forceinline__ float gated_value(float g, float u) { return (g <= 0.f ? 0.f : g) * u; }
 
+// Waits (again with a limit) for the last `issued` of a ring's loads to land: no
+// CTA leaves with copies into it under way, not even after a wait that gave up.
+// (stage, phase) is the place after the last one.
+template <int STAGES>
+__device__ __forceinline__ void wait_loads(uint64_t* full, int issued, int stage, uint32_t phase) {
+  for (int k = issued < STAGES ? issued : STAGES; k > 0; --k) {
+    const int s = stage - k;
+    if (!mbar_wait(&full[s < 0 ? s + STAGES : s], s < 0 ? phase ^ 1u : phase, nullptr)) break;
+  }
+}
+
+// Every wait is bounded.  A role whose wait gives up stops for good: the MMA
+// issuer once its MMAs in flight are done, the producer once its loads have
+// landed, and an epilogue warp writes NaN from then on (its later waits could
+// find an older phase of a barrier that nothing completes any more).
 // ---------------------------------------------------------------------------
 // One tile per CTA (128 channels x BT tokens, two accumulators when GATED); a
 // cluster of CTAs shares a tile's reduction, each taking a contiguous range of
@@ -129,10 +144,10 @@ __global__ void __launch_bounds__(192) int8_split_kernel(const __grid_constant__
 
   if (warp == 0) {
     if (lane == 0) {
-      int stage = 0;
+      int stage = 0, issued = 0;
       uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, nullptr)) break;
+      for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, nullptr, p.wait_limit_ns)) break;
         uint8_t* st = smem + stage * L::kStageBytes;
         mbar_arrive_expect_tx(&full[stage], L::kStageBytes);
         tma_load_2d(&tm_w, &full[stage], st, kb * kI8BK, n0);
@@ -140,15 +155,16 @@ __global__ void __launch_bounds__(192) int8_split_kernel(const __grid_constant__
         tma_load_2d(&tm_x, &full[stage], st + L::kStageBytes - L::kXBytes, kb * kI8BK, m0);
         if (++stage == L::kStages) { stage = 0; phase ^= 1u; }
       }
+      wait_loads<L::kStages>(full, issued, stage, phase);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_i8_s32(kI8ChannelTile, BT);
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&full[stage], phase, nullptr)) { ok = false; break; }
+      int stage = 0, last = -1;
+      uint32_t phase = 0, last_phase = 0;
+      bool ok = !p.lost;
+      for (int kb = kb0; kb < kb1 && ok; ++kb) {
+        if (!mbar_wait(&full[stage], phase, nullptr, p.wait_limit_ns)) { ok = false; break; }
         tc_fence_after();
         const uint32_t w = smem_u32(smem + stage * L::kStageBytes);
         const uint32_t x = w + L::kStageBytes - L::kXBytes;
@@ -160,9 +176,14 @@ __global__ void __launch_bounds__(192) int8_split_kernel(const __grid_constant__
           if (GATED) umma_i8(tmem_base + BT, smem_desc_sw128(w + L::kWBytes + k * 32, 16, 1024), xd, idesc, accum);
         }
         umma_commit(&empty[stage]);
+        last = stage;
+        last_phase = phase;
         if (++stage == L::kStages) { stage = 0; phase ^= 1u; }
       }
-      if (ok) umma_commit(tfull);
+      if (ok)
+        umma_commit(tfull);
+      else if (last >= 0)
+        mbar_wait(&empty[last], last_phase, nullptr);
     }
   } else {
     const int q = warp & 3;              // TMEM lane quadrant of this warp
@@ -174,7 +195,7 @@ __global__ void __launch_bounds__(192) int8_split_kernel(const __grid_constant__
     const float ws2 = GATED && n < p.N ? p.w2_scale[n] : 0.f;
     const float bias = !GATED && p.bias && n < p.N ? p.bias[n] : 0.f;
     named_bar_sync(1, 128);
-    if (!mbar_wait(tfull, 0, nullptr)) *failed = 1;
+    if (!mbar_wait(tfull, 0, nullptr, p.wait_limit_ns)) *failed = 1;
     __syncwarp();
     tc_fence_after();
     const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
@@ -355,7 +376,7 @@ __global__ void __launch_bounds__(Int8PairSmem::kThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      int stage = 0;
+      int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
       const void* tm_b = GATED && !leader ? &tm_b1 : &tm_b0;
@@ -365,7 +386,8 @@ __global__ void __launch_bounds__(Int8PairSmem::kThreads, 1)
         const int a0 = (GATED ? tok : ch) * 256 + static_cast<int>(rank) * 128;
         const int b0 = GATED ? ch * 128 : tok * 256 + static_cast<int>(rank) * 128;
         for (int kb = 0; kb < total_kb; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, nullptr)) { ok = false; break; }
+          if (!mbar_wait(&empty[stage], phase ^ 1u, nullptr, p.wait_limit_ns)) { ok = false; break; }
+          if (issued < L::kStages) ++issued;
           if (leader) mbar_arrive_expect_tx(&full[stage], 2 * L::kStageBytes);
           const uint32_t bar = mapa_shared(&full[stage], 0);
           uint8_t* st = smem + stage * L::kStageBytes;
@@ -374,21 +396,25 @@ __global__ void __launch_bounds__(Int8PairSmem::kThreads, 1)
           if (++stage == L::kStages) { stage = 0; phase ^= 1u; }
         }
       }
+      if (leader) wait_loads<L::kStages>(full, issued, stage, phase);  // both CTAs' loads: neither leaves before the other
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       constexpr uint32_t idesc = idesc_i8_s32(256, 256);
-      int stage = 0;
-      uint32_t phase = 0;
+      int stage = 0, last = -1;
+      uint32_t phase = 0, last_phase = 0;
       int it = 0;
       bool ok = true;
       for (int tile = cluster; tile < tiles && ok; tile += clusters, ++it) {
         const int acc = it & 1;
-        if (!mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, nullptr)) break;
+        if ((p.lost && it > 0) || !mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, nullptr, p.wait_limit_ns)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         const uint32_t d = tmem_base + acc * 256;
         for (int kb = 0; kb < total_kb; ++kb) {
-          if (!mbar_wait(&full[stage], phase, nullptr)) { ok = false; break; }
+          if (!mbar_wait(&full[stage], phase, nullptr, p.wait_limit_ns)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a = smem_u32(smem + stage * L::kStageBytes), b = a + L::kHalf;
 #pragma unroll
@@ -396,15 +422,19 @@ __global__ void __launch_bounds__(Int8PairSmem::kThreads, 1)
             umma_i8_pair(d, smem_desc_sw128(a + k * 32, 16, 1024), smem_desc_sw128(b + k * 32, 16, 1024), idesc,
                          (kb > 0 || k > 0) ? 1u : 0u);
           umma_commit_pair(&empty[stage]);
+          last = stage;
+          last_phase = phase;
           if (++stage == L::kStages) { stage = 0; phase ^= 1u; }
         }
         if (ok) umma_commit_pair(&tfull[acc]);
       }
+      if (!ok && last >= 0) mbar_wait(&empty[last], last_phase, nullptr);
     }
   } else {
     const int q = warp & 3, part = (warp - 2) >> 2, e = threadIdx.x - 64;
     const uint32_t tempty_leader[2] = {mapa_shared(&tempty[0], 0), mapa_shared(&tempty[1], 0)};
     TY* const y = static_cast<TY*>(p.y);
+    bool ok = true;
     int it = 0;
     for (int tile = cluster; tile < tiles; tile += clusters, ++it) {
       int tok, ch;
@@ -422,8 +452,7 @@ __global__ void __launch_bounds__(Int8PairSmem::kThreads, 1)
       const float rs = in ? (GATED ? p.x_scale : p.w_scale)[r] : 0.f;
       const float bias = !GATED && p.bias && in ? p.bias[r] : 0.f;
       named_bar_sync(1, 32 * L::kEpiWarps);
-      const bool ok = mbar_wait(&tfull[acc], (it >> 1) & 1, nullptr);
-      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&tfull[acc], (it >> 1) & 1, nullptr, p.wait_limit_ns));
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
       if (GATED) {
@@ -477,7 +506,7 @@ __global__ void __launch_bounds__(Int8PairSmem::kThreads, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive_cluster(tempty_leader[acc]);
+      if (ok) mbar_arrive_cluster(tempty_leader[acc]);
     }
   }
   tc_fence_before();

@@ -23,6 +23,8 @@ struct Int8GemmParams {
   int64_t ldy;
   int M, N, K;
   int y_type;
+  unsigned long long wait_limit_ns;  // of every wait for a barrier
+  bool lost;                         // test: MMAs are given up on (a tile of a CTA, all but a pair's first tile)
 };
 
 // How a product is cut: CTA pairs on 256 x 256 tiles, or tiles of 128 channels

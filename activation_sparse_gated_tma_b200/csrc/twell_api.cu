@@ -31,8 +31,8 @@ constexpr int kStaticUpdownMaxM = 256;
 thread_local char g_err[512] = "";
 thread_local int g_launches = 0;
 // One-shot fault injection (twell_test_expire_wait): the wait limit, in ns, of
-// the next fused-kernel launch on this thread, whose wait target is then made
-// unreachable; 0 = none.
+// the next fused-kernel or int8-product launch on this thread, in which
+// something waited for then never comes; 0 = none.
 thread_local long long g_expire_wait_ns = 0;
 // Route of the slotted rows in twell_ffn_bwd on this thread
 // (twell_bwd_slot_route): 0 by cost, 1 the dense-slot GEMMs, 2 the gather passes.
@@ -694,6 +694,9 @@ twell_status int8_product(const int8_t* x, int64_t ldx, const float* x_scale, co
   Int8GemmParams p = {};
   p.x_scale = x_scale; p.w_scale = w_scale; p.w2_scale = w2_scale; p.bias = bias;
   p.y = y; p.ldy = ldy; p.M = M; p.N = N; p.K = K; p.y_type = y_type;
+  p.lost = g_expire_wait_ns > 0;
+  p.wait_limit_ns = p.lost ? static_cast<unsigned long long>(g_expire_wait_ns) : kWaitLimitNs;
+  g_expire_wait_ns = 0;
   TW_CUDA(trace_begin(stream));
   TW_CUDA(launch_int8_gemm(plan, gated, tm_x, tm_w, tm_w2, p, dev.sms, stream));
   TW_CUDA(trace_end(stream, gated ? "int8_gated" : "int8_linear"));

@@ -355,7 +355,7 @@ twell_status twell_dequantize_rows(const int8_t* q, int64_t ldq, const float* sc
  * int8 (all values -128..127): 16-byte aligned, row strides multiples of 16; K
  * itself, M and N (up to 2^31 - 1025) may be any number.  bias [N] fp32 or
  * NULL.  No workspace.  Every wait inside is bounded; a tile whose wait gave up
- * is written as NaN.
+ * is written as NaN, and so is every later one of the same CTAs.
  */
 twell_status twell_int8_linear(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w, int64_t ldw,
                                const float* w_scale, const float* bias, int M, int N, int K, void* y,
@@ -393,7 +393,10 @@ twell_status twell_int8_cut(int token_tile, int k_splits);
  * TWELL_ERR_DEVICE_CHECK.  On a small batch the one-shot is taken instead by
  * the next twell_ffn_fused, whose grid barrier then waits for one CTA more
  * than the grid holds (y is left unwritten past the barrier).  The
- * small-batch twell_ffn_fwd has no such wait and leaves the one-shot armed.  The next twell_gate_pack clears the flag.  No
+ * small-batch twell_ffn_fwd has no such wait and leaves the one-shot armed.  The next twell_gate_pack clears the flag.
+ * A twell_int8_linear or twell_int8_gated that comes first takes the one-shot:
+ * its MMAs then stop (large products: after the first tile of each CTA pair)
+ * and the tiles not computed are written as NaN.  No
  * memory access changes.  limit_ns must lie in [1000, 1000000000]; 0 disarms.
  */
 twell_status twell_test_expire_wait(long long limit_ns);

@@ -168,3 +168,50 @@ def test_pairs_replayed_from_a_graph(cut):
         g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(ref, out))
+
+
+# ---------------------------------------------------------------- a wait that gives up
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_pairs_whose_wait_gave_up_write_nan_from_then_on(cut, gated, dtype):
+    # The MMAs stop after every pair's first tile (host-side injection, waits of 1 ms): those tiles are right, all later
+    # ones NaN, however often the accumulators' barriers would have turned over since; the next call is right again.
+    M, N, K = 5000, 5130, 640
+    x, xs = _operand(M, K, 1)
+    wg, gs = _operand(N, K, 2)
+    wu, us = _operand(N, K, 3)
+
+    def call():
+        return (tw.int8_gated(x, xs, wg, gs, wu, us, out_dtype=dtype) if gated
+                else tw.int8_linear(x, xs, wg, gs, out_dtype=dtype))
+    cut(*PAIRS)
+    good = call()
+    tw.test_expire_wait(1_000_000)
+    y = call()
+    torch.cuda.synchronize()
+    units = 128 if gated else 256
+    right = 0
+    for m in range(0, M, 256):
+        for n in range(0, N, units):
+            a, b = y[m:m + 256, n:n + units], good[m:m + 256, n:n + units]
+            whole = bool(torch.equal(a, b))
+            right += whole
+            assert whole or bool(a.isnan().all()), (m, n)
+    assert right == torch.cuda.get_device_properties(0).multi_processor_count // 2
+    assert torch.equal(call(), good)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("how", [(16, 1), (16, 4), (32, 2), (64, 1), (128, 1)])
+def test_tiles_whose_wait_gave_up_are_nan(cut, gated, how):
+    x, xs = _operand(70, 1000, 1)
+    wg, gs = _operand(300, 1000, 2)
+    wu, us = _operand(300, 1000, 3)
+
+    def call():
+        return tw.int8_gated(x, xs, wg, gs, wu, us) if gated else tw.int8_linear(x, xs, wg, gs)
+    cut(*how)
+    good = call()
+    tw.test_expire_wait(100_000)
+    assert bool(call().isnan().all())
+    assert torch.equal(call(), good)
