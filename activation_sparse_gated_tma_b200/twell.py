@@ -364,6 +364,7 @@ def dense_ffn_noalloc(x: torch.Tensor, wg_t: torch.Tensor, wu_t: torch.Tensor, w
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.int8: 3}  # twell_dtype
 _FLOATING = (torch.float32, torch.bfloat16, torch.float16)
 _I8 = (torch.int8,)
+_INT_MAX = 2 ** 31 - 1  # sizes are C ints
 
 
 def _elsewhere(stream, *tensors) -> bool:
@@ -404,6 +405,8 @@ def _rows(t: torch.Tensor, name: str, dtypes, shape=None) -> int:
         raise ValueError(f"{name} must be a matrix{'' if shape is None else f' of shape {tuple(shape)}'} of "
                          f"{' or '.join(map(str, dtypes))}, got {t.dtype} {tuple(size)}")
     rows, cols = size
+    if rows > _INT_MAX or cols > _INT_MAX:  # ctypes would cut them to 32 bits
+        raise ValueError(f"{name} must have at most {_INT_MAX} rows and columns, got {tuple(size)}")
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name}'s elements of a row must be contiguous (strides {t.stride()})")

@@ -132,3 +132,18 @@ def test_ctypes_signatures_cover_the_new_calls():
     for n in ("twell_layer_norm_fwd", "twell_layer_norm_int8", "twell_layer_norm_bwd", "twell_quantize_rows",
               "twell_dequantize_rows", "twell_int8_linear", "twell_int8_gated"):
         assert n in tw.header_functions() and getattr(L, n).argtypes[-1] is ctypes.c_void_p, n
+
+
+@pytest.mark.parametrize("shape", [((1 << 32) + 5, 2), (2, (1 << 32) + 5), (1 << 31, 1)])
+def test_wrappers_refuse_sizes_past_32_bits(shape):
+    # The library takes sizes as 32-bit integers; cut to those, 2^32 + 5 rows would be 5.
+    M, D = shape
+    z, i8 = torch.empty(shape, device="meta"), torch.empty(shape, dtype=torch.int8, device="meta")
+    v, d = torch.empty(M, device="meta"), torch.empty(D, device="meta")
+    few, one = torch.empty((3, D), dtype=torch.int8, device="meta"), torch.empty(3, device="meta")
+    for call in (lambda: tw.layer_norm(z, d, d), lambda: tw.layer_norm_int8(z, d, d), lambda: tw.quantize_rows(z),
+                 lambda: tw.layer_norm_bwd(z, z, v, v), lambda: tw.dequantize_rows(i8, v),
+                 lambda: tw.int8_linear(i8, v, few, one), lambda: tw.int8_linear(few, one, i8, v),
+                 lambda: tw.int8_gated(few, one, i8, v, i8, v)):
+        with pytest.raises(ValueError, match="2147483647"):
+            call()
