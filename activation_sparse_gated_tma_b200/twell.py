@@ -650,12 +650,17 @@ def int8_ffn_weights(wg_t: torch.Tensor, wu_t: torch.Tensor, wd: torch.Tensor) -
 
 
 def dense_ffn_int8(x: torch.Tensor, weights: Int8FFN, norm=None, out_dtype: torch.dtype = torch.float32,
-                   stream=None) -> torch.Tensor:
+                   stream=None, h_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The dense FFN (dense_ffn) in 8-bit integers: x's rows quantised, the
     gated pair of products, h's rows quantised, the down product.  norm =
-    (weight, bias, eps) applies the layer norm to x first (layer_norm_int8)."""
+    (weight, bias, eps) applies the layer norm to x first (layer_norm_int8).
+
+    h is held in h_dtype between its product and its quantisation: bfloat16
+    halves the bytes, and its half step of 2^-9 to 2^-8 of a value stays below
+    the int8 half step of 1/254 of the row's largest; with float32 h is rounded
+    once, to int8 (float16 rows may pass that type's range)."""
     q, s = quantize_rows(x, stream) if norm is None else layer_norm_int8(x, *norm, stream=stream)
-    h = int8_gated(q, s, weights.wg, weights.wg_scale, weights.wu, weights.wu_scale, stream=stream)
+    h = int8_gated(q, s, weights.wg, weights.wg_scale, weights.wu, weights.wu_scale, out_dtype=h_dtype, stream=stream)
     q, s = quantize_rows(h, stream)
     return int8_linear(q, s, weights.wd_t, weights.wd_scale, out_dtype=out_dtype, stream=stream)
 

@@ -214,3 +214,22 @@ def test_norm_sparse_ffn_and_both_backward_passes():
     for got, want in ((dx, rx), (dnw, (up * hat).sum(0)), (dnb, up.sum(0))):
         # the rule of the FFN's own gradients, whose error the norm passes on
         assert float((got.double() - want).abs().max()) <= 2e-2 * float(want.pow(2).mean().sqrt())
+
+
+@pytest.mark.parametrize("M", [5, 300])
+@pytest.mark.parametrize("h_dtype", [F32, BF16, F16])
+def test_dense_ffn_int8_hidden_rows_of_any_type(M, h_dtype):
+    K, N = 256, 1024
+    _, _, dev = _ffn_inputs(M, K, N, 3)
+    W = tw.int8_ffn_weights(dev["wg_t"], dev["wu_t"], dev["wd"])
+    y = tw.dense_ffn_int8(dev["x"], W, h_dtype=h_dtype)
+    # As test_dense_ffn_int8, with the half step of h's type.
+    q, s = tw.quantize_rows(dev["x"])
+    h = _product64(q, s, W.wg, W.wg_scale).clamp_min(0) * _product64(q, s, W.wu, W.wu_scale)
+    wd = W.wd_t.double() * W.wd_scale.double()[:, None]
+    off = _half_step(h_dtype, h) + 8 * U * h.abs() + h.abs().amax(1, keepdim=True) / 127 * 0.51
+    _check(y, h @ wd.t(), off @ wd.abs().t() + 5 * U * (h.abs() @ wd.abs().t()))
+    # The int8 rows themselves are those of the fp32 (or rounded) h.
+    hh = tw.int8_gated(q, s, W.wg, W.wg_scale, W.wu, W.wu_scale, out_dtype=h_dtype)
+    q2, s2 = tw.quantize_rows(hh)
+    assert torch.equal(y, tw.int8_linear(q2, s2, W.wd_t, W.wd_scale, out_dtype=F32))
