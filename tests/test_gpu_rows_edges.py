@@ -181,3 +181,58 @@ def test_threads_that_differentiate_rows_of_different_lengths(lengths):
     _in_threads(calls, 5000)
     for x, mean, rstd, dx in keep[::2]:   # (dw is left out: two threads use one scratch)
         assert torch.equal(dx, tw.layer_norm_bwd(x, x, mean, rstd, param_grads=False)[0])
+
+
+# ---------------------------------------------------------------- more rows than groups
+@pytest.mark.parametrize("M,D,gap", [(5000, 256, 0), (5000, 2560, 0), (2500, 8192, 0), (1300, 16384, 0),      # aligned
+                                     (5003, 255, 0), (5001, 2047, 0), (5000, 2559, 1), (2500, 8191, 0), (1300, 16383, 0)])
+@pytest.mark.parametrize("tx,ty", [(F32, BF16), (BF16, BF16), (F16, F32)])
+def test_layer_norm_of_many_rows(M, D, gap, tx, ty):
+    # Every group of warps takes several rows in turn.
+    x = _rows(M, D, tx, gap)
+    w, b = _affine(D, F32)
+    y, mean, rstd = tw.layer_norm(x, w, b, EPS, out_dtype=ty, stats=True)
+    _check_norm(y, mean, rstd, x, w, b)
+    # (By 64-bit quotients of fp32 results: those have the kernel's own values, which the tests above check.)
+    y = tw.layer_norm(x, w, b, EPS, out_dtype=F32)
+    q, scale = tw.layer_norm_int8(x, w, b, EPS)
+    ref, s = _quant64(y)
+    # The same fp32 operations; were one fused otherwise, y would be off by 8 u of its terms, and q by one step at ties.
+    hat = (x.double() - mean.double()[:, None]).abs() * rstd.double()[:, None]
+    e = 8 * U * (w.double().abs() * hat + b.double().abs())
+    top = e.amax(1)
+    assert bool(((scale.double() - s.double()).abs() <= (top + 2 * U * s.double() * 127) / 127).all())
+    at = y.double() / s.double()[:, None]
+    assert bool(((q.double() - at).abs() <= 0.5 + (e + top[:, None]) / s.double()[:, None] + 1e-4).all())
+
+
+@pytest.mark.parametrize("M,K,gap", [(5000, 256, 0), (5001, 2047, 0), (4000, 5632, 0), (4000, 5631, 1), (1300, 20480, 0),
+                                     (1300, 20479, 0), (700, 20481, 0), (650, 40001, 0)])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_quantize_rows_of_many_rows(M, K, gap, dtype):
+    # (Rows of more than 20480 elements are read twice, a block each: 592 blocks.)
+    x = _rows(M, K, dtype, gap)
+    q, scale = tw.quantize_rows(x)
+    for i in range(0, M, 1000):
+        part = slice(i, i + 1000)
+        ref, s = _quant64(x[part])
+        assert torch.equal(q[part].double(), ref) and torch.equal(scale[part], s)
+    for t in (F32, BF16):
+        assert torch.equal(tw.dequantize_rows(q, scale, t), (q.float() * scale[:, None]).to(t))
+
+
+@pytest.mark.parametrize("M,D", [(2500, 8192), (2500, 8191), (5001, 2047), (1300, 16384)])
+def test_layer_norm_of_many_rows_some_far_from_zero(M, D):
+    # Groups take rows with and without the correction's two sums in turn.
+    x = _rows(M, D, F32)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    far = torch.rand(M, generator=g, device="cuda") < 0.4
+    level = torch.where(torch.rand(M, generator=g, device="cuda") < 0.5, 6016.0, -1234.567)
+    x[far] = level[far, None]
+    w, b = _affine(D, F32)
+    y, mean, rstd = tw.layer_norm(x, w, b, EPS, stats=True)
+    assert torch.equal(y[far], b.expand(int(far.sum()), D)) and torch.equal(mean[far], x[far, 0])
+    _check_norm(y[~far], mean[~far], rstd[~far], x[~far], w, b)
+    q, scale = tw.layer_norm_int8(x, w, b, EPS)
+    ref, s = _quant64(b[None])
+    assert torch.equal(q[far].double(), ref.expand(int(far.sum()), D)) and bool((scale[far] == s).all())
