@@ -67,6 +67,7 @@ __device__ __forceinline__ void wait_loads(uint64_t* full, int issued, int stage
 // issuer once its MMAs in flight are done, the producer once its loads have
 // landed, and an epilogue warp writes NaN from then on (its later waits could
 // find an older phase of a barrier that nothing completes any more).
+
 // ---------------------------------------------------------------------------
 // One tile per CTA (128 channels x BT tokens, two accumulators when GATED); a
 // cluster of CTAs shares a tile's reduction, each taking a contiguous range of

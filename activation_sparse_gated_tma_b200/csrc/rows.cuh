@@ -7,9 +7,9 @@
 // depend on its length is kept small: a row belongs to as few warps as hold it
 // (one up to 2560 columns for the norm), more only while rows are too few for
 // the warps; 16-byte loads and stores, and 16 to 32 warps per SM, are all the
-// memory parallelism it takes.  Measured at 16384 x 2560: norm bf16 to bf16 33 us
-// (5.1 TB/s; five warps per row 68, rows through a shared-memory ring of bulk
-// copies 36), fp32 to bf16 45 us (5.7 TB/s), bf16 to int8 40 us; at 8192 x 5632,
+// memory parallelism it takes.  Measured at 16384 x 2560: norm bf16 to bf16 32 us
+// (5.2 TB/s; five warps per row 68, rows through a shared-memory ring of bulk
+// copies 36), fp32 to bf16 45 us (5.6 TB/s), bf16 to int8 40 us; at 8192 x 5632,
 // bf16 to int8 rows 24 us (5.7 TB/s) and back 25.
 //
 // Columns of thread t in a group of T threads, layer j < NC, i < 8: 8 (t + j T) + i.
@@ -570,7 +570,8 @@ __global__ void __launch_bounds__(kRowThreads, norm_blocks(NC))
     float rstd = rsqrtf(sum_of(plus_square) * p.inv_d + p.eps);
     // This mean is off by a few 2^-24 of itself: where it is far above the spread, by much of a deviation (or so much
     // that the squares pass the range and leave no rstd).  The deviations' own mean, off by as little of itself, takes
-    // that off again.  The whole group does or does not; other rows do not pay for the two more sums.
+    // that off again.  The whole group does or does not.  (fp32 to bf16 16384 x 2560 takes 42 us whether all rows do or
+    // none; the check itself costs bf16 65536 x 256 18.8 us for 17.9, 8192 x 4096 32.1 for 30.7, 16384 x 2560 nothing.)
     if (fabsf(mean) * rstd > 4.f || rstd == 0.f) {
       const float off = sum_of([](float s, float d) { return s + d; }) / static_cast<float>(p.D);
       mean += off;

@@ -12,7 +12,7 @@ constexpr int kMaxGroups = 8;        // rows that a block works on at once
 constexpr int kMaxGroupWarps = 8;    // of a row
 constexpr int kNormChunks = 10;      // of eight elements that a thread holds at most
 // Joining the pieces of unaligned rows wants more warps (bf16, 8191 x 1535: 30 us with 6 chunks, 25 with 5; 8191 x 4095:
-// 66 with 8, 54), unless so all rows are at work at once (2047 x 1535: 7.3 us with 6, 8.1 with 5).
+// 66 with 8, 55), unless so all rows are at work at once (2047 x 1535: 7.3 us with 6, 8.1 with 5).
 constexpr int norm_chunks_unaligned(int M, int sms) { return M <= 16 * sms ? 6 : 5; }
 constexpr int kQuantizeChunks = 6;   // as long as kMaxGroupWarps warps hold the row so
 constexpr int kNormFewWarps = 8;     // per SM, up to which a row is spread over more warps than hold it

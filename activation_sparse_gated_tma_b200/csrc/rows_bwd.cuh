@@ -5,9 +5,9 @@
 // columns), and what a row costs beyond its columns is shared by R rows at a time
 // (two where the registers allow): their 2 R sums go through one exchange and one barrier.  x and dy are
 // read straight into registers, several rows' worth of bytes in flight per SM.
-// Bound by HBM for fp32 rows: 16384 x 2560 takes 84 us (6.0 TB/s; batches of
+// Bound by HBM for fp32 rows: 16384 x 2560 takes 85 us (5.9 TB/s; batches of
 // rows through a shared-memory ring and two passes over each took 93).  Of
-// 16-bit rows (bf16 x, fp32 dy: 69 us) a row's chain of load, exchange and store
+// 16-bit rows (bf16 x, fp32 dy: 70 us) a row's chain of load, exchange and store
 // takes as long as its bytes: halving the fp32 instructions (two values each)
 // changed nothing.
 // Rows are dealt to groups in a fixed way, so the order of every sum depends on

@@ -41,8 +41,9 @@ struct RowShape {
 // The fewest warps per row whose lanes hold it in `most` chunks each; more
 // while twice as many warps leave every SM no more than `few` of them. A row's
 // warps meet at a barrier, so the norm, with two sums to join, gains from more
-// warps up to 8 an SM (bf16 1000 x 2560: 8.1 us, with 32 9.3) and the
-// quantisation, with one maximum, up to 32 (2.9 us; a form of it that took 5.7 with 8 took 4.3).
+// warps up to 8 an SM (bf16 1000 x 2560: 8.3 us; with 32 it took 9.3 where 8 took
+// 8.1) and the quantisation, with one maximum, up to 32 (1000 x 2560: 4.3 us
+// against 5.7 with 8, and 2.9 since).
 inline RowShape row_shape(int M, int D, int most, int few, int sms) {
   RowShape r;
   r.warps = 1;

@@ -321,6 +321,9 @@ twell_status twell_layer_norm_int8(const void* x, twell_dtype x_type, int64_t ld
  * with xh = (x - mean) rstd and g = dy weight,
  *   dx = rstd (g - (sum g + xh sum g xh) / D)      of x_type,
  *   dweight [D] = sum over rows of dy xh, dbias [D] = sum over rows of dy,  fp32.
+ * These two are added row after row in up to a few hundred groups of rows, then
+ * over the groups, in fp32: their error grows with M / groups, about 2^-24 of
+ * the terms' magnitudes for each row of a group at worst.
  * dweight and dbias may each be NULL.  scratch: device memory of at least
  * twell_layer_norm_bwd_scratch_bytes(M, D) bytes, 16-byte aligned (one partial
  * row of both sums per group of rows); unused when both are NULL.  The size
